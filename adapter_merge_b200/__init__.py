@@ -13,6 +13,7 @@ from typing import Optional, Sequence
 __all__ = [
     "AdafuseError", "lib", "library_path", "pregate", "segments", "Plan", "PointerArrays",
     "RENORM", "POOL_MEAN", "STATUS_BAD_INDEX", "STATUS_TIMEOUT", "PLAN_Y_F32", "round_bf16",
+    "project", "gated_project", "epilogue", "rotary", "rotary_frequencies",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -31,6 +32,12 @@ STATUS_BAD_INDEX = 1 << 0
 STATUS_TIMEOUT = 1 << 1
 PLAN_Y_F32 = 1 << 0
 PLAN_TEST_STALL = 1 << 31
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+OUT_F32 = 1 << 4
+IN_F32 = 1 << 5
+PAIRS = 1 << 6
+POS_I32 = 1 << 7
+TEST_STALL = 1 << 31
 
 # Every entry point the header declares.
 EXPORTS = (
@@ -38,7 +45,8 @@ EXPORTS = (
     "adafuse_switch", "adafuse_merge_per_linear", "adafuse_segments",
     "adafuse_apply_workspace_bytes", "adafuse_apply", "adafuse_plan_status",
     "adafuse_plan_last_launches", "adafuse_strerror", "adafuse_version",
-    "adafuse_apply_noalloc", "adafuse_round_bf16",
+    "adafuse_apply_noalloc", "adafuse_round_bf16", "adafuse_project", "adafuse_gated_project",
+    "adafuse_epilogue", "adafuse_rotary",
 )
 
 
@@ -55,6 +63,15 @@ class Linear(ctypes.Structure):
         ("A", ctypes.c_void_p), ("B", ctypes.c_void_p),
         ("d_out", ctypes.c_int32), ("d_in", ctypes.c_int32),
         ("a_expert_stride", ctypes.c_int64), ("b_expert_stride", ctypes.c_int64),
+    ]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [
+        ("in_", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("in_token_stride", ctypes.c_int64), ("in_head_stride", ctypes.c_int64),
+        ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+        ("weight", ctypes.c_void_p), ("heads", ctypes.c_int32),
     ]
 
 
@@ -87,6 +104,11 @@ def lib():
     L.adafuse_apply.argtypes = [P, P, P, i64, P, P, i32, P, ctypes.c_size_t, P]
     L.adafuse_apply_noalloc.argtypes = [P, P, P, i64, P, P, i32, P]
     L.adafuse_round_bf16.argtypes = [P, P, i64, P]
+    L.adafuse_project.argtypes = [P, i64, i32, i64, P, i32, i64, P, P, i64, P, i64, u32, P, P]
+    L.adafuse_gated_project.argtypes = [P, i64, i32, i64, P, P, i32, i64, P, P, P, i64, u32, P, P]
+    L.adafuse_epilogue.argtypes = [P, i64, i64, i64, P, P, i64, P, i64, P, i64, u32, P]
+    L.adafuse_rotary.argtypes = [ctypes.POINTER(Heads), ctypes.POINTER(Heads), i64, i32, i32, P, P,
+                                 ctypes.c_float, ctypes.c_float, u32, P]
     L.adafuse_plan_status.argtypes = [P, P, ctypes.POINTER(i32)]
     L.adafuse_plan_last_launches.argtypes = [P]
     L.adafuse_plan_last_launches.restype = i32
@@ -157,6 +179,275 @@ def round_bf16(src, out=None, stream=None):
         raise ValueError("round_bf16 writes a contiguous bf16 tensor of src's size")
     _check(lib().adafuse_round_bf16(_ptr(src), _ptr(out), src.numel(), _stream(stream)), "adafuse_round_bf16")
     return out
+
+
+# ---------------------------------------------------------------- operators
+# The operators between the adapted linears.  Each runs on its tensors' device
+# and, unless `stream` is given, on that device's current stream; a result that
+# the call allocates belongs to the stream it is computed on.
+
+def _rows(name: str, t, dtypes, shape=None, device=None):
+    """Checks a [rows, n] operand with unit stride along its rows; returns its row stride."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} is {t.dtype}; expected {' or '.join(map(str, dtypes))}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected "
+                         f"{'two dimensions' if shape is None else tuple(shape)}")
+    rows, inner = t.stride()
+    if inner != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name}: the elements of a row must be adjacent (strides {t.stride()})")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+    return rows
+
+
+def _vector(name: str, t, dtype, n: int, device):
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: expected {n} adjacent elements of {dtype}, got {t.dtype} {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+    return t.data_ptr()
+
+
+def _activation(name) -> int:
+    try:
+        return ACTIVATIONS[name]
+    except (KeyError, TypeError):
+        raise ValueError(f"activation {name!r} is none of {[a for a in ACTIVATIONS if a]}") from None
+
+
+class _On:
+    """Runs a call on `device` and `stream`: sets both for what it allocates,
+    where they are not the current ones, and gives the raw stream."""
+
+    def __init__(self, device, stream):
+        import torch
+        self._undo = None
+        if device.type != "cuda":
+            raise ValueError(f"expected CUDA tensors, got {device}")
+        if stream is not None:
+            raw = stream if isinstance(stream, int) else stream.cuda_stream
+            self._undo = torch.cuda.stream(torch.cuda.ExternalStream(raw, device=device) if raw
+                                           else torch.cuda.default_stream(device))
+            self._undo.__enter__()
+            self.raw = raw
+        else:
+            if device.index is not None and device.index != torch.cuda.current_device():
+                self._undo = torch.cuda.device(device)
+                self._undo.__enter__()
+            self.raw = torch.cuda.current_stream(device).cuda_stream
+
+    def done(self):
+        if self._undo is not None:
+            self._undo.__exit__(None, None, None)
+
+
+def _status_ptr(status, device):
+    import torch
+    if status is None:
+        return None
+    if status.dtype != torch.int32 or status.numel() < 1 or status.device != device:
+        raise ValueError("status is one int32 on the call's device")
+    return status.data_ptr()
+
+
+def project(x, W, bias=None, activation=None, residual=None, out=None, out_dtype=None, status=None, stream=None):
+    """act(x W^T + bias) + residual in one launch, e.g. with a W_out that
+    Plan.merge wrote: x bf16 [T, d_in], W bf16 [d_out, d_in], bias bf16 [d_out],
+    residual bf16 [T, d_out] (rows may be strided or one expanded row; may be
+    `out` itself).  activation: "relu", "silu", "gelu", "gelu_tanh" or None.
+    Returns `out`, bf16 [T, d_out]; out_dtype=torch.float32 leaves the fp32
+    result unrounded (a row-parallel rank's partial sums).  STATUS_TIMEOUT is
+    OR-ed into `status` (int32 [1]) when a device-side wait gave up."""
+    import torch
+    bf16 = torch.bfloat16
+    dev = x.device
+    ldx = _rows("x", x, (bf16,))
+    T, K = x.shape
+    ldw = _rows("W", W, (bf16,), None, dev)
+    N = W.shape[0]
+    if W.shape[1] != K:
+        raise ValueError(f"x has {K} columns and W {W.shape[1]}")
+    kind = out.dtype if out is not None else out_dtype or bf16
+    if kind not in (bf16, torch.float32) or (out_dtype is not None and kind != out_dtype):
+        raise ValueError("the result is bfloat16 or float32")
+    b = _vector("bias", bias, bf16, N, dev)
+    flags = _activation(activation) | (0 if kind is bf16 else OUT_F32)
+    ldr = 0 if residual is None else _rows("residual", residual, (bf16,), (T, N), dev)
+    ldy = N if out is None else _rows("out", out, (kind,), (T, N), dev)
+    s = _status_ptr(status, dev)
+    on = _On(dev, stream)
+    try:
+        if out is None:
+            out = torch.empty((T, N), dtype=kind, device=dev)
+        _check(lib().adafuse_project(x.data_ptr(), T, K, ldx, W.data_ptr(), N, ldw, b, _ptr(residual), ldr,
+                                     out.data_ptr(), ldy, flags, s, on.raw), "adafuse_project")
+    finally:
+        on.done()
+    return out
+
+
+def gated_project(x, W_gate, W_up, bias_gate=None, bias_up=None, activation="silu", out=None, status=None,
+                  stream=None):
+    """act(x W_gate^T + bias_gate) * (x W_up^T + bias_up) in one launch: the
+    feed-forward block's two projections, activation and product.  Weights bf16
+    [d_out, d_in] with the same row stride; everything else as project."""
+    import torch
+    bf16 = torch.bfloat16
+    dev = x.device
+    ldx = _rows("x", x, (bf16,))
+    T, K = x.shape
+    ldw = _rows("W_gate", W_gate, (bf16,), None, dev)
+    N = W_gate.shape[0]
+    if W_gate.shape[1] != K:
+        raise ValueError(f"x has {K} columns and W_gate {W_gate.shape[1]}")
+    if _rows("W_up", W_up, (bf16,), (N, K), dev) != ldw and N > 1:
+        raise ValueError("W_gate and W_up need the same row stride")
+    bg, bu = _vector("bias_gate", bias_gate, bf16, N, dev), _vector("bias_up", bias_up, bf16, N, dev)
+    flags = _activation(activation)
+    ldy = N if out is None else _rows("out", out, (bf16,), (T, N), dev)
+    s = _status_ptr(status, dev)
+    on = _On(dev, stream)
+    try:
+        if out is None:
+            out = torch.empty((T, N), dtype=bf16, device=dev)
+        _check(lib().adafuse_gated_project(x.data_ptr(), T, K, ldx, W_gate.data_ptr(), W_up.data_ptr(), N, ldw, bg,
+                                           bu, out.data_ptr(), ldy, flags, s, on.raw), "adafuse_gated_project")
+    finally:
+        on.done()
+    return out
+
+
+def epilogue(y, bias=None, activation=None, up=None, residual=None, out=None, out_dtype=None, stream=None):
+    """act(y + bias) * up + residual of outputs that exist already, in one
+    launch, rounded once: silu(gate) * up of an unmerged apply, an apply's
+    output plus the residual stream, or all-reduced fp32 sums.  y and up
+    [T, n], both bf16 or both fp32; bias bf16 [n]; residual bf16 [T, n].  Rows
+    may be strided, those of y, up and residual one expanded row.  Returns
+    `out`, bf16 [T, n] (or fp32); it may be y, up or residual itself."""
+    import torch
+    bf16, f32 = torch.bfloat16, torch.float32
+    dev = y.device
+    ldy = _rows("y", y, (bf16, f32))
+    T, n = y.shape
+    kind = out.dtype if out is not None else out_dtype or bf16
+    if kind not in (bf16, f32) or (out_dtype is not None and kind != out_dtype):
+        raise ValueError("the result is bfloat16 or float32")
+    b = _vector("bias", bias, bf16, n, dev)
+    ldu = 0 if up is None else _rows("up", up, (y.dtype,), (T, n), dev)
+    ldr = 0 if residual is None else _rows("residual", residual, (bf16,), (T, n), dev)
+    ldo = n if out is None else _rows("out", out, (kind,), (T, n), dev)
+    flags = _activation(activation) | (IN_F32 if y.dtype is f32 else 0) | (OUT_F32 if kind is f32 else 0)
+    on = _On(dev, stream)
+    try:
+        if out is None:
+            out = torch.empty((T, n), dtype=kind, device=dev)
+        _check(lib().adafuse_epilogue(y.data_ptr(), T, n, ldy, b, _ptr(up), ldu, _ptr(residual), ldr, out.data_ptr(),
+                                      ldo, flags, on.raw), "adafuse_epilogue")
+    finally:
+        on.done()
+    return out
+
+
+def rotary_frequencies(dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                       original_length: int = 4096, fast_turns: float = 32.0, slow_turns: float = 1.0, device=None):
+    """(freq fp64 [dim/2], value factor) for `rotary`: freq[i] = base^(-2i/dim)
+    radians per position, scaled for contexts `factor` times as long:
+      None          as they are
+      "linear"      every frequency divided by the factor (positions squeezed)
+      "base"        the base times factor^(dim / (dim - 2)): the slowest pair is
+                    slowed by the factor, the fastest keeps its frequency
+      "wavelength"  by the turns that a pair makes within original_length
+                    positions: at least fast_turns keeps its frequency, at most
+                    slow_turns is slowed by the factor, a linear ramp over the
+                    pairs between; rotated values are scaled by
+                    0.1 ln(factor) + 1 (Peng et al. 2023, "YaRN")."""
+    import math
+
+    import torch
+    if dim < 2 or dim % 2:
+        raise ValueError(f"dim {dim} is not a positive even number")
+    if base <= 0 or factor <= 0:
+        raise ValueError("base and factor are positive")
+    i = torch.arange(0, dim, 2, dtype=torch.float64)
+    if scaling == "base":
+        if dim == 2:
+            raise ValueError("scaling by the base needs more than one pair")
+        base = base * factor ** (dim / (dim - 2))
+    freq, mult = base ** (-i / dim), 1.0
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "wavelength":
+        if base == 1 or original_length < 1 or not fast_turns > slow_turns > 0:
+            raise ValueError("scaling by wavelength needs a base other than 1, original_length >= 1 and "
+                             "fast_turns > slow_turns > 0")
+        pair = lambda turns: dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+        lo, hi = max(math.floor(pair(fast_turns)), 0), min(math.ceil(pair(slow_turns)), dim // 2 - 1)
+        ramp = ((i / 2 - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        freq = freq / factor * ramp + freq * (1 - ramp)
+        mult = 0.1 * math.log(factor) + 1 if factor > 1 else 1.0
+    elif scaling not in (None, "base"):
+        raise ValueError(f"scaling {scaling!r} is none of None, 'linear', 'base', 'wavelength'")
+    return freq.to(device) if device is not None else freq, mult
+
+
+def _heads(name: str, t, out, weight, D, T, dev):
+    import torch
+    bf16 = torch.bfloat16
+    for what, m in ((name, t), (name + "_out", out)):
+        if m.dtype != bf16 or m.dim() != 3 or m.shape[0] != T or m.shape[2] != D or m.shape[1] != t.shape[1]:
+            raise ValueError(f"{what}: expected bfloat16 [{T}, heads, {D}], got {m.dtype} {tuple(m.shape)}")
+        if m.stride(2) != 1 and D > 1:
+            raise ValueError(f"{what}: the elements of a head must be adjacent (strides {m.stride()})")
+        if m.device != dev:
+            raise ValueError(f"{what} is on {m.device}, not {dev}")
+    a, b = t.stride(), out.stride()
+    return Heads(t.data_ptr(), out.data_ptr(), a[0], a[1], b[0], b[1],
+                 _vector(name + "_weight", weight, bf16, D, dev), t.shape[1])
+
+
+def rotary(q, k, positions, freq, layout: str = "half", factor: float = 1.0, q_weight=None, k_weight=None,
+           eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+    """Rotates queries and keys by their positions, after an RMS norm of each
+    head where a weight is given, in one launch.  q bf16 [T, heads, D], k
+    likewise (or None), any token and head strides; positions int64 or int32
+    [T], any sign; freq fp64 [rot/2] (rotary_frequencies), rot <= D: the
+    elements from rot on are not rotated.  layout "half" rotates elements i and
+    i + rot/2, "interleaved" 2i and 2i + 1; `factor` scales the rotated
+    elements.  q_weight / k_weight bf16 [D].  Returns (q_out, k_out), new
+    contiguous tensors unless given; q_out may be q itself, k_out k."""
+    import torch
+    dev = q.device
+    if q.dim() != 3 or (k is not None and k.dim() != 3):
+        raise ValueError("q and k have three dimensions: tokens, heads, elements")
+    T, _, D = q.shape
+    if layout not in ("half", "interleaved"):
+        raise ValueError(f"layout {layout!r} is neither 'half' nor 'interleaved'")
+    if positions.dtype not in (torch.int64, torch.int32) or tuple(positions.shape) != (T,) or \
+            (T > 1 and positions.stride(0) != 1) or positions.device != dev:
+        raise ValueError(f"positions: expected {T} adjacent int64 or int32 on {dev}")
+    if freq.dim() != 1:
+        raise ValueError("freq has one dimension")
+    f = _vector("freq", freq, torch.float64, freq.shape[0], dev)
+    if k is None and (k_weight is not None or k_out is not None):
+        raise ValueError("k_weight and k_out go with k")
+    flags = (PAIRS if layout == "interleaved" else 0) | (POS_I32 if positions.dtype is torch.int32 else 0)
+    on = _On(dev, stream)
+    try:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+        hq = _heads("q", q, q_out, q_weight, D, T, dev)
+        hk = None if k is None else _heads("k", k, k_out, k_weight, D, T, dev)
+        _check(lib().adafuse_rotary(ctypes.byref(hq), None if hk is None else ctypes.byref(hk), T, D,
+                                    2 * freq.shape[0], positions.data_ptr(), f, factor, eps, flags, on.raw),
+               "adafuse_rotary")
+    finally:
+        on.done()
+    return q_out, k_out
 
 
 class Plan:

@@ -1,0 +1,435 @@
+// Projections with their epilogue:
+//   y = act(x W^T + bias) + residual                                (project)
+//   y = act(x W_gate^T + bias_gate) * (x W_up^T + bias_up)          (gated)
+// for x [T, d_in] and weights [d_out, d_in], everything in fp32 up to the one
+// rounding of y.
+//
+// stream_kernel: W streams once per tile of tokens, T up to a few hundred.
+// A unit is 128 rows of W (and the same 128 of W_up) against a tile of up to
+// 256 (128) tokens, with the W rows as the M side of the tensor-core product
+// and the tokens, padded to 16, as its N side, so that a single token costs
+// one pass over W.  A unit's d_in is split over the CTAs of a cluster: one
+// warp loads the CTA's range of 64-column chunks through a ring of shared
+// memory by TMA, one issues tcgen05.mma into TMEM, then the partial sums go
+// to shared memory (token by token), and each CTA adds up its share of the
+// tokens over the cluster's partials, always in rank order, applies the
+// epilogue and writes y.  No workspace, no counters, no atomics.  TMEM is
+// freed before a CTA waits for its cluster, so no CTA ever waits for another
+// while it holds TMEM that the other needs.
+//
+// The tensor core rounds each step of an accumulator towards zero, which adds
+// up over long sums (measured against 64 bits: 4.4e-6 relative at d_in = 4096,
+// 1.6e-5 at 13824).  bf16 outputs round a thousand times coarser; fp32 outputs
+// accumulate parts of at most 512 columns in accumulators of their own, added
+// up in registers.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstring>
+
+#include "act.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace af {
+namespace {
+
+constexpr int kStreamThreads = 192;                     // producer, MMA, four epilogue warps
+constexpr int kMaxRing = 12;
+constexpr int kMaxSplits = 8;
+constexpr uint32_t kWTile = kTileM * kChunkK * 2;       // 16 KB
+constexpr int kPartCols = 512;                          // columns per accumulator of an fp32 output
+
+struct StreamArgs {
+    void* y;
+    const uint16_t* residual;
+    const uint16_t* bias;
+    const uint16_t* bias_up;
+    int32_t* status;
+    int64_t ldy, ldr, T;
+    int32_t N;              // d_out
+    int32_t tile;           // tokens per unit: a multiple of 16
+    int32_t n_tt;           // token tiles
+    int32_t chunks, splits, ring, parts;
+    uint32_t tmem_cols, stage_bytes, act;
+    int32_t y_f32, stall;
+};
+
+// bias, activation, product and residual of 8 consecutive outputs, and their store
+template <bool kGated>
+__device__ __forceinline__ void finish8(const StreamArgs& a, float (&v)[8], float (&u)[8], int64_t t, int o)
+{
+    const auto add = [](float (&d)[8], const uint16_t* p) {
+        const uint4 w = *reinterpret_cast<const uint4*>(p);
+        d[0] += bf16lo(w.x); d[1] += bf16hi(w.x); d[2] += bf16lo(w.y); d[3] += bf16hi(w.y);
+        d[4] += bf16lo(w.z); d[5] += bf16hi(w.z); d[6] += bf16lo(w.w); d[7] += bf16hi(w.w);
+    };
+    if (a.bias) add(v, a.bias + o);
+    if (a.act != ADAFUSE_ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = activate(v[i], a.act);
+    }
+    if constexpr (kGated) {
+        if (a.bias_up) add(u, a.bias_up + o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= u[i];
+    } else {
+        if (a.residual) add(v, a.residual + t * a.ldr + o);
+    }
+    if (!kGated && a.y_f32) {
+        float* p = static_cast<float*>(a.y) + t * a.ldy + o;
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(a.y) + t * a.ldy + o;
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    }
+}
+
+template <bool kGated>
+__global__ void __launch_bounds__(kStreamThreads) stream_kernel(const __grid_constant__ CUtensorMap xmap,
+                                                                const __grid_constant__ CUtensorMap wmap,
+                                                                const __grid_constant__ CUtensorMap umap,
+                                                                const StreamArgs a)
+{
+    extern __shared__ uint8_t dyn[];
+    __shared__ uint64_t full[kMaxRing], empty[kMaxRing], done;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = a.splits > 1 ? (int)cluster_rank() : 0;
+    const int unit = (int)blockIdx.x / a.splits;
+    const int row0 = unit / a.n_tt * kTileM;
+    const int64_t t0 = (int64_t)(unit % a.n_tt) * a.tile;
+    const int ntok = (int)min((int64_t)a.tile, a.T - t0);
+    const int c0 = (int)((int64_t)a.chunks * rank / a.splits);
+    const int n = (int)((int64_t)a.chunks * (rank + 1) / a.splits) - c0;
+
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int i = 0; i < a.ring; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(&done, 1);
+        fence_mbar_init();
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    if (warp == 1) {
+        tmem_alloc(&tmem_slot, a.tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int issued = 0;
+            for (int i = 0; i < n; ++i) {
+                const int s = i % a.ring;
+                if (i >= a.ring && !mbar_wait(&empty[s], (uint32_t)(i / a.ring - 1) & 1, &abort_flag)) break;
+                if (a.stall && blockIdx.x == 0 && i == 0) continue;         // test hook: never arrives
+                uint8_t* p = ring + (size_t)s * a.stage_bytes;
+                const int k = (c0 + i) * kChunkK;
+                mbar_arrive_expect_tx(&full[s], a.stage_bytes);
+                tma_load_2d(p, &wmap, &full[s], k, row0);
+                if constexpr (kGated) tma_load_2d(p + kWTile, &umap, &full[s], k, row0);
+                tma_load_2d(p + (kGated ? 2 : 1) * kWTile, &xmap, &full[s], k, (int)t0);
+                issued = i + 1;
+            }
+            // a wait gave up: what is in flight has to land before shared memory is given back
+            if (abort_flag)
+                for (int i = max(0, issued - a.ring); i < issued; ++i)
+                    if (!(a.stall && blockIdx.x == 0 && i == 0))
+                        mbar_wait_landed(&full[i % a.ring], (uint32_t)(i / a.ring) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = make_idesc_bf16(kTileM, (uint32_t)a.tile, 0u, 0u);
+            int part = -1;
+            for (int i = 0; i < n; ++i) {
+                const int s = i % a.ring;
+                if (!mbar_wait(&full[s], (uint32_t)(i / a.ring) & 1, &abort_flag)) break;
+                tc_fence_after();
+                const uint32_t w = smem_u32(ring + (size_t)s * a.stage_bytes);
+                const uint32_t x = w + (kGated ? 2 : 1) * kWTile;
+                const int now = (int)((int64_t)i * a.parts / n);
+                const bool fresh = now != part;
+                part = now;
+                const uint32_t d = tmem + (uint32_t)(part * a.tile);
+#pragma unroll
+                for (int kk = 0; kk < kChunkK / 16; ++kk) {
+                    const uint64_t bdesc = make_sdesc(x + kk * 32u, 16u, 1024u, kLayoutSw128);
+                    const uint32_t acc = fresh && kk == 0 ? 0u : 1u;
+                    tc_mma_bf16(d, make_sdesc(w + kk * 32u, 16u, 1024u, kLayoutSw128), bdesc, idesc, acc);
+                    if constexpr (kGated)
+                        tc_mma_bf16(d + (uint32_t)a.tile, make_sdesc(w + kWTile + kk * 32u, 16u, 1024u, kLayoutSw128),
+                                    bdesc, idesc, acc);
+                }
+                tc_commit(&empty[s]);
+            }
+            tc_commit(&done);
+            if (abort_flag) mbar_wait_landed(&done, 0);
+        }
+        __syncwarp();
+    }
+
+    // The partial sums, [token][128 rows] fp32, over the ring: every load has
+    // been consumed once the last product is done.
+    float* part = reinterpret_cast<float*>(ring);
+    if (warp >= 2) {
+        const bool ok = mbar_wait(&done, 0, &abort_flag) && !*(volatile int*)&abort_flag;
+        if (__all_sync(0xffffffffu, ok)) {
+            tc_fence_after();
+            const int q = warp & 3;
+            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+#pragma unroll
+            for (int m = 0; m < (kGated ? 2 : 1); ++m) {
+                float* p = part + m * a.tile * kTileM + q * 32 + lane;
+                for (int t = 0; t < ntok; t += 16) {
+                    uint32_t v[16];
+                    float sum[16];
+                    tc_ld_x16(lanes + (uint32_t)(m * a.tile + t), v);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sum[i] = __uint_as_float(v[i]);
+                    for (int j = 1; j < a.parts; ++j) {
+                        tc_ld_x16(lanes + (uint32_t)(j * a.tile + t), v);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) sum[i] += __uint_as_float(v[i]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) p[(t + i) * kTileM] = sum[i];
+                }
+            }
+            tc_fence_before();
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, a.tmem_cols);
+    }
+    if (a.splits > 1) cluster_sync();
+
+    // Groups of 8 rows of W (outputs) of one token, spread over the cluster.
+    const uint32_t base = smem_u32(part);
+    const bool fine = !*(volatile int*)&abort_flag;
+    for (int g = rank * kStreamThreads + (int)threadIdx.x; g < ntok * (kTileM / 8); g += a.splits * kStreamThreads) {
+        const int t = g / (kTileM / 8), o = (g & (kTileM / 8 - 1)) * 8;
+        if (row0 + o >= a.N) continue;
+        float v[8] = {}, u[8] = {};
+        const uint32_t at = base + (uint32_t)(t * kTileM + o) * 4u;
+        if (a.splits > 1) {
+#pragma unroll
+            for (int r = 0; r < kMaxSplits; ++r) {
+                if (r >= a.splits) break;
+                const uint32_t p = cluster_map(at, (uint32_t)r);
+                const float4 x0 = ld_cluster_v4(p), x1 = ld_cluster_v4(p + 16);
+                v[0] += x0.x; v[1] += x0.y; v[2] += x0.z; v[3] += x0.w;
+                v[4] += x1.x; v[5] += x1.y; v[6] += x1.z; v[7] += x1.w;
+                if constexpr (kGated) {
+                    const uint32_t pu = p + (uint32_t)(a.tile * kTileM) * 4u;
+                    const float4 y0 = ld_cluster_v4(pu), y1 = ld_cluster_v4(pu + 16);
+                    u[0] += y0.x; u[1] += y0.y; u[2] += y0.z; u[3] += y0.w;
+                    u[4] += y1.x; u[5] += y1.y; u[6] += y1.z; u[7] += y1.w;
+                }
+            }
+        } else {
+            const float* p = part + t * kTileM + o;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = p[i];
+                if constexpr (kGated) u[i] = p[a.tile * kTileM + i];
+            }
+        }
+        if (fine) finish8<kGated>(a, v, u, t0 + t, row0 + o);
+    }
+    if (threadIdx.x == 0 && !fine && a.status) atomicOr(a.status, ADAFUSE_STATUS_TIMEOUT);
+    if (a.splits > 1) cluster_sync();       // the others may still read this CTA's partials
+}
+
+// ------------------------------------------------------------------ host side
+
+// bf16 [rows, cols] with rows `ld` elements apart, boxes of 64 columns x box_rows, 128-byte swizzle
+bool encode_rows(CUtensorMap* m, const void* p, int64_t rows, int32_t cols, int64_t ld, int box_rows)
+{
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)(rows > 1 ? ld : cols) * 2};
+    cuuint32_t box[2] = {kChunkK, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box,
+                                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Shared memory per CTA of the two ways to run the stream kernel: two CTAs on
+// an SM, or one.
+constexpr uint32_t kSmemHalf = 111 * 1024, kSmemFull = 225 * 1024;
+
+// Clusters of `splits` CTAs that the device runs at a time, asked once.
+template <bool kGated>
+int clusters_at_once(int dev, int splits, bool half)
+{
+    static std::atomic<int> known[16][2][kMaxSplits + 1];
+    std::atomic<int>* slot = dev < 16 ? &known[dev][half][splits] : nullptr;
+    int v = slot ? slot->load(std::memory_order_relaxed) : 0;
+    if (v > 0) return v;
+    auto kernel = stream_kernel<kGated>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemFull) != cudaSuccess)
+        return 0;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)splits);
+    cfg.blockDim = dim3(kStreamThreads);
+    cfg.dynamicSmemBytes = half ? kSmemHalf : kSmemFull;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&v, kernel, &cfg) != cudaSuccess || v < 1) return 0;
+    if (slot) slot->store(v, std::memory_order_relaxed);
+    return v;
+}
+
+struct Call {
+    const void *x, *W, *W_up;
+    int64_t ldx, ldw;
+    int32_t K;
+    StreamArgs a;
+    cudaStream_t s;
+};
+
+template <bool kGated>
+int launch_stream(Call& c)
+{
+    StreamArgs& a = c.a;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ADAFUSE_ERR_DEVICE;
+    a.chunks = (c.K + kChunkK - 1) / kChunkK;
+    // the fewest token tiles, of equal height
+    const int most = kGated ? 128 : 256;
+    a.n_tt = (int)((a.T + most - 1) / most);
+    a.tile = (int)(((a.T + a.n_tt - 1) / a.n_tt + 15) / 16 * 16);
+    const auto ring_of = [&](bool half) {
+        a.stage_bytes = (kGated ? 2 : 1) * kWTile + (uint32_t)a.tile * kChunkK * 2;
+        return (int)std::min<uint32_t>(kMaxRing, ((half ? kSmemHalf : kSmemFull) - 1024) / a.stage_bytes);
+    };
+    // Two CTAs per SM keep more units in flight; taller tiles need the whole
+    // shared memory for four stages and their partial sums.
+    const bool half = a.tile <= 64;
+    a.ring = ring_of(half);
+    // The split of d_in that ends first: as many rounds of clusters as the
+    // device needs, each as long as its chunks and a fixed part.
+    const int64_t blocks = (int64_t)((a.N + kTileM - 1) / kTileM) * a.n_tt;
+    double best = 0;
+    a.splits = 0;
+    for (int S = 1; S <= kMaxSplits && S <= a.chunks; ++S) {
+        const int at_once = clusters_at_once<kGated>(dev, S, half);
+        if (!at_once) continue;
+        const double cost = (double)((blocks + at_once - 1) / at_once) * ((a.chunks + S - 1) / S + 6);
+        if (!a.splits || cost < best) best = cost, a.splits = S;
+    }
+    if (!a.splits) return ADAFUSE_ERR_CUDA;
+    a.parts = 1;
+    if (a.y_f32) {
+        const int per = (a.chunks + a.splits - 1) / a.splits;
+        a.parts = std::min((half ? 256 : 512) / a.tile, (per * kChunkK + kPartCols - 1) / kPartCols);
+        a.parts = std::max(1, std::min(a.parts, a.chunks / a.splits));
+    }
+    a.tmem_cols = 32;
+    while ((int)a.tmem_cols < a.tile * a.parts * (kGated ? 2 : 1)) a.tmem_cols *= 2;
+    if (blocks * a.splits > 0x7fffffff) return ADAFUSE_ERR_UNSUPPORTED;
+
+    CUtensorMap xm, wm, um;
+    if (!encode_rows(&xm, c.x, a.T, c.K, c.ldx, a.tile) || !encode_rows(&wm, c.W, a.N, c.K, c.ldw, kTileM))
+        return ADAFUSE_ERR_UNSUPPORTED;
+    if (!kGated) um = wm;
+    else if (!encode_rows(&um, c.W_up, a.N, c.K, c.ldw, kTileM)) return ADAFUSE_ERR_UNSUPPORTED;
+    return launch_pdl_cluster(stream_kernel<kGated>, dim3((unsigned)(blocks * a.splits)), dim3(kStreamThreads),
+                              half ? kSmemHalf : kSmemFull, a.splits, c.s, xm, wm, um, a);
+}
+
+int check(Call& c, const void* bias, const void* bias_up, bool gated, uint32_t flags)
+{
+    StreamArgs& a = c.a;
+    const uint32_t act = flags & ADAFUSE_ACT_MASK;
+    if (flags & ~(ADAFUSE_ACT_MASK | ADAFUSE_TEST_STALL | (gated ? 0u : ADAFUSE_OUT_F32))) return ADAFUSE_ERR_INVALID_ARG;
+    if (a.T < 0 || c.K < 1 || a.N < 1) return ADAFUSE_ERR_INVALID_ARG;
+    if (act > ADAFUSE_ACT_GELU_TANH || c.K % 8 || a.N % 8 || a.T > 0x7fffffff) return ADAFUSE_ERR_UNSUPPORTED;
+    if (a.T == 0) return ADAFUSE_OK;
+    if (!c.x || !c.W || !a.y || (gated && !c.W_up)) return ADAFUSE_ERR_INVALID_ARG;
+    a.y_f32 = flags & ADAFUSE_OUT_F32 ? 1 : 0;
+    const int64_t size = a.y_f32 ? 4 : 2;
+    if (a.T == 1) { c.ldx = c.K; a.ldy = a.ldr = a.N; }
+    if (a.N == 1) c.ldw = c.K;
+    if (!a.residual) a.ldr = 0;
+    if (c.ldx < c.K || c.ldw < c.K || a.ldy < a.N || (a.ldr != 0 && a.ldr < a.N)) return ADAFUSE_ERR_INVALID_ARG;
+    for (const void* p : {c.x, c.W, c.W_up, (const void*)a.y, (const void*)a.residual, bias, bias_up})
+        if (!aligned_to(p, 16)) return ADAFUSE_ERR_UNSUPPORTED;
+    if (c.ldx % 8 || c.ldw % 8 || a.ldr % 8 || a.ldy % (a.y_f32 ? 4 : 8)) return ADAFUSE_ERR_UNSUPPORTED;
+    if (c.ldx >= (1ll << 38) || c.ldw >= (1ll << 38)) return ADAFUSE_ERR_UNSUPPORTED;      // tensor-map strides
+    const RowSpan y{a.y, a.T, a.N * size, a.ldy * size};
+    const RowSpan in[] = {{c.x, a.T, 2ll * c.K, 2 * c.ldx}, {c.W, a.N, 2ll * c.K, 2 * c.ldw},
+                          {c.W_up, a.N, 2ll * c.K, 2 * c.ldw}, {bias, 1, 2ll * a.N, 2ll * a.N},
+                          {bias_up, 1, 2ll * a.N, 2ll * a.N}, {a.residual, a.T, 2ll * a.N, 2 * a.ldr}};
+    for (const RowSpan& r : in) {
+        const bool in_place = &r == &in[5] && r.base == a.y && !a.y_f32 && a.ldr == a.ldy;
+        if (r.base && !in_place && rows_overlap(y, r)) return ADAFUSE_ERR_INVALID_ARG;
+    }
+    a.bias = static_cast<const uint16_t*>(bias);
+    a.bias_up = static_cast<const uint16_t*>(bias_up);
+    a.act = act;
+    a.stall = flags & ADAFUSE_TEST_STALL ? 1 : 0;
+    if (!device_sms()) return ADAFUSE_ERR_DEVICE;
+    if (!tensor_map_encoder()) return ADAFUSE_ERR_CUDA;
+    return ADAFUSE_OK;
+}
+
+}  // namespace
+}  // namespace af
+
+using namespace af;
+
+extern "C" int adafuse_project(const void* x, int64_t T, int32_t d_in, int64_t x_row_stride, const void* W,
+                               int32_t d_out, int64_t w_row_stride, const void* bias, const void* residual,
+                               int64_t r_row_stride, void* y, int64_t y_row_stride, uint32_t flags, int32_t* status,
+                               adafuse_stream_t stream)
+{
+    Call c{x, W, nullptr, x_row_stride, w_row_stride, d_in, {}, (cudaStream_t)stream};
+    c.a.y = y;
+    c.a.residual = static_cast<const uint16_t*>(residual);
+    c.a.ldy = y_row_stride;
+    c.a.ldr = r_row_stride;
+    c.a.T = T;
+    c.a.N = d_out;
+    c.a.status = status;
+    const int rc = check(c, bias, nullptr, false, flags);
+    if (rc || T == 0) return rc;
+    return launch_stream<false>(c);
+}
+
+extern "C" int adafuse_gated_project(const void* x, int64_t T, int32_t d_in, int64_t x_row_stride,
+                                     const void* W_gate, const void* W_up, int32_t d_out, int64_t w_row_stride,
+                                     const void* bias_gate, const void* bias_up, void* y, int64_t y_row_stride,
+                                     uint32_t flags, int32_t* status, adafuse_stream_t stream)
+{
+    Call c{x, W_gate, W_up, x_row_stride, w_row_stride, d_in, {}, (cudaStream_t)stream};
+    c.a.y = y;
+    c.a.ldy = y_row_stride;
+    c.a.T = T;
+    c.a.N = d_out;
+    c.a.status = status;
+    const int rc = check(c, bias_gate, bias_up, true, flags);
+    if (rc || T == 0) return rc;
+    return launch_stream<true>(c);
+}

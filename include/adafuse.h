@@ -300,6 +300,129 @@ ADAFUSE_API int adafuse_apply_noalloc(adafuse_plan* plan, const void* const* x_p
  */
 ADAFUSE_API int adafuse_round_bf16(const float* in, void* out, int64_t n, adafuse_stream_t stream);
 
+/* ---- operators between the adapted linears ----
+ *
+ * A decoder layer's work next to the targeted linears, for the merged weights
+ * (adafuse_project, adafuse_gated_project) and for outputs that adafuse_apply
+ * or an all-reduce has left (adafuse_epilogue), and the rotation of queries and
+ * keys (adafuse_rotary).  None has a counterpart on the pages, which decode
+ * with the fused weights (page pt section 2.B) and leave the layer to the
+ * backbone.  They take no plan and no workspace, run on the current device,
+ * are one launch each, and can be captured into a graph.  T == 0 is valid and
+ * launches nothing.  An output may not overlap an input, except where a call
+ * says that it may be the same buffer.
+ */
+
+/* flags: the activation, in the low bits of `flags` */
+#define ADAFUSE_ACT_NONE        0u
+#define ADAFUSE_ACT_RELU        1u          /* max(v, 0); NaN stays */
+#define ADAFUSE_ACT_SILU        2u          /* v / (1 + exp(-v)) */
+#define ADAFUSE_ACT_GELU        3u          /* v (1 + erf(v / sqrt 2)) / 2 */
+#define ADAFUSE_ACT_GELU_TANH   4u          /* v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2 */
+#define ADAFUSE_ACT_MASK        7u
+#define ADAFUSE_OUT_F32         (1u << 4)   /* the output is fp32, unrounded, instead of bf16 */
+#define ADAFUSE_IN_F32          (1u << 5)   /* epilogue: y and up are fp32 instead of bf16 */
+#define ADAFUSE_PAIRS           (1u << 6)   /* rotary: rotate elements (2i, 2i+1) instead of (i, i + rot/2) */
+#define ADAFUSE_POS_I32         (1u << 7)   /* rotary: positions are int32 instead of int64 */
+#define ADAFUSE_TEST_STALL      (1u << 31)  /* project, gated_project: as ADAFUSE_PLAN_TEST_STALL, for this call */
+
+/*
+ * Projection: y[t, :] = act(x[t, :] W^T + bias) + residual[t, :], the products
+ * and everything after them in fp32, rounded once to bf16 (with
+ * ADAFUSE_OUT_F32 not at all: a row-parallel rank's partial sums; sums over
+ * more than 512 columns are then added up in parts, so that the result keeps
+ * close to fp32's precision).
+ *   x         bf16 [T, d_in], rows x_row_stride elements apart
+ *   W         bf16 [d_out, d_in], rows w_row_stride apart: e.g. a W_out that
+ *             adafuse_merge wrote
+ *   bias      bf16 [d_out] or NULL
+ *   residual  bf16 [T, d_out] or NULL, rows r_row_stride apart (0: one row for
+ *             all tokens); may be y itself (same address and stride, bf16)
+ *   y         bf16 (fp32) [T, d_out], rows y_row_stride apart
+ *   status    int32 [1] (device, nullable): ADAFUSE_STATUS_TIMEOUT is OR-ed in
+ *             when a wait gave up (y is then incomplete)
+ * d_in and d_out are multiples of 8; x, W, residual and y are 16-byte aligned
+ * and their strides multiples of 8 elements (y fp32: of 4); the bias is
+ * 16-byte aligned.
+ * Errors: INVALID_ARG (null pointers, T < 0, sizes < 1, unknown flags, a stride
+ * shorter than its row with T > 1, overlapping buffers), UNSUPPORTED
+ * (alignment, multiples, an activation that is not listed, T over 2^31 - 1),
+ * DEVICE, CUDA.
+ */
+ADAFUSE_API int adafuse_project(const void* x, int64_t T, int32_t d_in, int64_t x_row_stride, const void* W,
+                                int32_t d_out, int64_t w_row_stride, const void* bias, const void* residual,
+                                int64_t r_row_stride, void* y, int64_t y_row_stride, uint32_t flags,
+                                int32_t* status, adafuse_stream_t stream);
+
+/*
+ * The feed-forward block's gated pair of projections:
+ *   y[t, :] = act(x[t, :] W_gate^T + bias_gate) * (x[t, :] W_up^T + bias_up),
+ * both products in one kernel, in fp32, rounded once to bf16.  W_gate and W_up
+ * bf16 [d_out, d_in] share w_row_stride; the biases (bf16 [d_out]) are NULL or
+ * not independently.  Everything else, and the errors, as adafuse_project
+ * (no residual, no ADAFUSE_OUT_F32).
+ */
+ADAFUSE_API int adafuse_gated_project(const void* x, int64_t T, int32_t d_in, int64_t x_row_stride,
+                                      const void* W_gate, const void* W_up, int32_t d_out, int64_t w_row_stride,
+                                      const void* bias_gate, const void* bias_up, void* y, int64_t y_row_stride,
+                                      uint32_t flags, int32_t* status, adafuse_stream_t stream);
+
+/*
+ * The same epilogue on outputs that exist already:
+ *   out[t, :] = act(y[t, :] + bias) * up[t, :] + residual[t, :]
+ * in fp32, rounded once: adafuse_apply's gate and up outputs, its outputs and
+ * the residual stream, or the all-reduced fp32 sums of a row-parallel layer.
+ *   y         bf16 (ADAFUSE_IN_F32: fp32) [T, n]
+ *   bias      bf16 [n] or NULL
+ *   up        y's type [T, n] or NULL;  residual  bf16 [T, n] or NULL
+ *   out       bf16 (ADAFUSE_OUT_F32: fp32) [T, n]; may be y, up or residual
+ *             itself (same address, stride and type)
+ * The row strides are in elements; those of y, up and residual may be 0 (one
+ * row for all tokens).  Any n, stride and alignment of whole elements; rows of
+ * 16-byte aligned groups of 8 elements move in 16-byte accesses.
+ * Errors: INVALID_ARG (as above), UNSUPPORTED (an activation that is not
+ * listed, n over 2^31 - 1).
+ */
+ADAFUSE_API int adafuse_epilogue(const void* y, int64_t T, int64_t n, int64_t y_row_stride, const void* bias,
+                                 const void* up, int64_t up_row_stride, const void* residual, int64_t r_row_stride,
+                                 void* out, int64_t out_row_stride, uint32_t flags, adafuse_stream_t stream);
+
+/* Heads of one kind (queries, or keys) as adafuse_rotary reads and writes them:
+ * head h of token t starts token_stride*t + head_stride*h elements in. */
+typedef struct {
+    const void* in;             /* bf16 */
+    void*       out;            /* bf16; may be `in` (same address and strides) */
+    int64_t     in_token_stride, in_head_stride;
+    int64_t     out_token_stride, out_head_stride;
+    const void* weight;         /* bf16 [head_dim]: norm each head first; NULL: no norm */
+    int32_t     heads;
+} adafuse_heads;
+
+/*
+ * Rotation of queries and keys by their positions, after an optional norm of
+ * each head, in one pass:
+ *   v = weight ? head * weight / sqrt(mean(head^2) + eps) : head
+ *   (v_a, v_b) -> factor * (v_a cos - v_b sin, v_a sin + v_b cos),
+ *   with the angle positions[t] * freq[i]
+ * for the pairs (a, b) = (i, i + rot/2) or, with ADAFUSE_PAIRS, (2i, 2i + 1),
+ * i < rot/2; the elements from rot on are not rotated.  Everything between the
+ * bf16 input and the one rounding of the output is fp32, the angle excepted:
+ * it is reduced to one turn in 64-bit integers, so far positions lose nothing.
+ *   q, k       HOST structs; k may be NULL
+ *   positions  int64 (ADAFUSE_POS_I32: int32) [T], any sign: rotating by -p
+ *              undoes a rotation by p
+ *   freq       fp64 [rot/2], radians per position, as adafuse's callers scale
+ *              them for long contexts;  factor scales the rotated elements
+ * Outputs may not overlap inputs other than their own, nor each other (both
+ * may live in one buffer, e.g. rows that hold q, k and v of a token).
+ * Errors: INVALID_ARG (null pointers, sizes, unknown flags, overlapping
+ * outputs), UNSUPPORTED (rot odd or > head_dim, head_dim > 1024, over 2^16
+ * heads), CUDA.
+ */
+ADAFUSE_API int adafuse_rotary(const adafuse_heads* q, const adafuse_heads* k, int64_t T, int32_t head_dim,
+                               int32_t rot, const void* positions, const double* freq, float factor, float eps,
+                               uint32_t flags, adafuse_stream_t stream);
+
 /*
  * Synchronise `stream`, read the plan's device status word into
  * *device_status (host) and clear it.  Returns ADAFUSE_ERR_TIMEOUT if the
