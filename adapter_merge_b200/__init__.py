@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 __all__ = [
@@ -107,7 +108,7 @@ def lib():
     L.adafuse_project.argtypes = [P, i64, i32, i64, P, i32, i64, P, P, i64, P, i64, u32, P, P]
     L.adafuse_gated_project.argtypes = [P, i64, i32, i64, P, P, i32, i64, P, P, P, i64, u32, P, P]
     L.adafuse_epilogue.argtypes = [P, i64, i64, i64, P, P, i64, P, i64, P, i64, u32, P]
-    L.adafuse_rotary.argtypes = [ctypes.POINTER(Heads), ctypes.POINTER(Heads), i64, i32, i32, P, P,
+    L.adafuse_rotary.argtypes = [P, P, i64, i32, i32, P, P,
                                  ctypes.c_float, ctypes.c_float, u32, P]
     L.adafuse_plan_status.argtypes = [P, P, ctypes.POINTER(i32)]
     L.adafuse_plan_last_launches.argtypes = [P]
@@ -184,31 +185,33 @@ def round_bf16(src, out=None, stream=None):
 # ---------------------------------------------------------------- operators
 # The operators between the adapted linears.  Each runs on its tensors' device
 # and, unless `stream` is given, on that device's current stream; a result that
-# the call allocates belongs to the stream it is computed on.
+# the call allocates belongs to the stream it is computed on.  A decode step
+# makes these calls for one token, so the checks ask each tensor once.
 
-def _rows(name: str, t, dtypes, shape=None, device=None):
+def _rows(name: str, t, dtype, shape, dev: int) -> int:
     """Checks a [rows, n] operand with unit stride along its rows; returns its row stride."""
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} is {t.dtype}; expected {' or '.join(map(str, dtypes))}")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected "
-                         f"{'two dimensions' if shape is None else tuple(shape)}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}; expected {dtype} {tuple(shape)}"
+                         f"{'' if dev < 0 else f' on cuda:{dev}'}")
     rows, inner = t.stride()
-    if inner != 1 and t.shape[1] > 1:
+    if inner != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the elements of a row must be adjacent (strides {t.stride()})")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not {device}")
     return rows
 
 
-def _vector(name: str, t, dtype, n: int, device):
+def _vector(name: str, t, dtype, n: int, dev: int):
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name}: expected {n} adjacent elements of {dtype}, got {t.dtype} {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not {device}")
+    if t.dtype is not dtype or t.shape != (n,) or t.get_device() != dev or (t.stride(0) != 1 and n > 1):
+        raise ValueError(f"{name}: expected {n} adjacent elements of {dtype} on the call's device, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
+
+
+def _matrix(name: str, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected two dimensions")
+    return t.shape
 
 
 def _activation(name) -> int:
@@ -218,39 +221,41 @@ def _activation(name) -> int:
         raise ValueError(f"activation {name!r} is none of {[a for a in ACTIVATIONS if a]}") from None
 
 
-class _On:
-    """Runs a call on `device` and `stream`: sets both for what it allocates,
-    where they are not the current ones, and gives the raw stream."""
-
-    def __init__(self, device, stream):
-        import torch
-        self._undo = None
-        if device.type != "cuda":
-            raise ValueError(f"expected CUDA tensors, got {device}")
-        if stream is not None:
-            raw = stream if isinstance(stream, int) else stream.cuda_stream
-            self._undo = torch.cuda.stream(torch.cuda.ExternalStream(raw, device=device) if raw
-                                           else torch.cuda.default_stream(device))
-            self._undo.__enter__()
-            self.raw = raw
-        else:
-            if device.index is not None and device.index != torch.cuda.current_device():
-                self._undo = torch.cuda.device(device)
-                self._undo.__enter__()
-            self.raw = torch.cuda.current_stream(device).cuda_stream
-
-    def done(self):
-        if self._undo is not None:
-            self._undo.__exit__(None, None, None)
-
-
-def _status_ptr(status, device):
+def _result_type(out, out_dtype):
     import torch
-    if status is None:
-        return None
-    if status.dtype != torch.int32 or status.numel() < 1 or status.device != device:
-        raise ValueError("status is one int32 on the call's device")
-    return status.data_ptr()
+    kind = out.dtype if out is not None else out_dtype or torch.bfloat16
+    if kind not in (torch.bfloat16, torch.float32) or (out_dtype is not None and kind != out_dtype):
+        raise ValueError("the result is bfloat16 or float32")
+    return kind
+
+
+def _on(dev: int, stream):
+    """(raw stream, context): the stream a call on device `dev` goes to, and,
+    where device or stream are not the current ones, a context that makes them
+    so for what the call allocates (else None)."""
+    import torch
+    if dev < 0:
+        raise ValueError("expected CUDA tensors")
+    if stream is None:
+        if dev == torch.cuda.current_device():
+            return torch._C._cuda_getCurrentRawStream(dev), None
+        return torch._C._cuda_getCurrentRawStream(dev), torch.cuda.device(dev)
+    raw = stream if isinstance(stream, int) else stream.cuda_stream
+    device = torch.device("cuda", dev)
+    return raw, torch.cuda.stream(torch.cuda.ExternalStream(raw, device=device) if raw
+                                  else torch.cuda.default_stream(device))
+
+
+def _call(name: str, ctx, shape, kind, dev: int, out, args):
+    """One library call: args(out, raw pointer of out); allocates `out` if None."""
+    import torch
+    if ctx is not None:
+        with ctx:
+            return _call(name, None, shape, kind, dev, out, args)
+    if out is None:
+        out = torch.empty(shape, dtype=kind, device=dev)
+    _check(args(out.data_ptr()), name)
+    return out
 
 
 def project(x, W, bias=None, activation=None, residual=None, out=None, out_dtype=None, status=None, stream=None):
@@ -262,31 +267,21 @@ def project(x, W, bias=None, activation=None, residual=None, out=None, out_dtype
     result unrounded (a row-parallel rank's partial sums).  STATUS_TIMEOUT is
     OR-ed into `status` (int32 [1]) when a device-side wait gave up."""
     import torch
-    bf16 = torch.bfloat16
-    dev = x.device
-    ldx = _rows("x", x, (bf16,))
-    T, K = x.shape
-    ldw = _rows("W", W, (bf16,), None, dev)
-    N = W.shape[0]
-    if W.shape[1] != K:
-        raise ValueError(f"x has {K} columns and W {W.shape[1]}")
-    kind = out.dtype if out is not None else out_dtype or bf16
-    if kind not in (bf16, torch.float32) or (out_dtype is not None and kind != out_dtype):
-        raise ValueError("the result is bfloat16 or float32")
-    b = _vector("bias", bias, bf16, N, dev)
+    bf16, dev = torch.bfloat16, x.get_device()
+    (T, K), N = _matrix("x", x), _matrix("W", W)[0]
+    ldx, ldw = _rows("x", x, bf16, (T, K), dev), _rows("W", W, bf16, (N, K), dev)
+    kind = bf16 if out is None and out_dtype is None else _result_type(out, out_dtype)
+    b = None if bias is None else _vector("bias", bias, bf16, N, dev)
+    r = ldr = ldy = None
+    if residual is not None:
+        r, ldr = residual.data_ptr(), _rows("residual", residual, bf16, (T, N), dev)
+    if out is not None:
+        ldy = _rows("out", out, kind, (T, N), dev)
+    s = None if status is None else _vector("status", status, torch.int32, 1, dev)
     flags = _activation(activation) | (0 if kind is bf16 else OUT_F32)
-    ldr = 0 if residual is None else _rows("residual", residual, (bf16,), (T, N), dev)
-    ldy = N if out is None else _rows("out", out, (kind,), (T, N), dev)
-    s = _status_ptr(status, dev)
-    on = _On(dev, stream)
-    try:
-        if out is None:
-            out = torch.empty((T, N), dtype=kind, device=dev)
-        _check(lib().adafuse_project(x.data_ptr(), T, K, ldx, W.data_ptr(), N, ldw, b, _ptr(residual), ldr,
-                                     out.data_ptr(), ldy, flags, s, on.raw), "adafuse_project")
-    finally:
-        on.done()
-    return out
+    raw, ctx = _on(dev, stream)
+    return _call("adafuse_project", ctx, (T, N), kind, dev, out, lambda y: lib().adafuse_project(
+        x.data_ptr(), T, K, ldx, W.data_ptr(), N, ldw, b, r, ldr or 0, y, N if ldy is None else ldy, flags, s, raw))
 
 
 def gated_project(x, W_gate, W_up, bias_gate=None, bias_up=None, activation="silu", out=None, status=None,
@@ -295,29 +290,18 @@ def gated_project(x, W_gate, W_up, bias_gate=None, bias_up=None, activation="sil
     feed-forward block's two projections, activation and product.  Weights bf16
     [d_out, d_in] with the same row stride; everything else as project."""
     import torch
-    bf16 = torch.bfloat16
-    dev = x.device
-    ldx = _rows("x", x, (bf16,))
-    T, K = x.shape
-    ldw = _rows("W_gate", W_gate, (bf16,), None, dev)
-    N = W_gate.shape[0]
-    if W_gate.shape[1] != K:
-        raise ValueError(f"x has {K} columns and W_gate {W_gate.shape[1]}")
-    if _rows("W_up", W_up, (bf16,), (N, K), dev) != ldw and N > 1:
+    bf16, dev = torch.bfloat16, x.get_device()
+    (T, K), N = _matrix("x", x), _matrix("W_gate", W_gate)[0]
+    ldx, ldw = _rows("x", x, bf16, (T, K), dev), _rows("W_gate", W_gate, bf16, (N, K), dev)
+    if _rows("W_up", W_up, bf16, (N, K), dev) != ldw and N > 1:
         raise ValueError("W_gate and W_up need the same row stride")
     bg, bu = _vector("bias_gate", bias_gate, bf16, N, dev), _vector("bias_up", bias_up, bf16, N, dev)
+    ldy = N if out is None else _rows("out", out, bf16, (T, N), dev)
+    s = None if status is None else _vector("status", status, torch.int32, 1, dev)
     flags = _activation(activation)
-    ldy = N if out is None else _rows("out", out, (bf16,), (T, N), dev)
-    s = _status_ptr(status, dev)
-    on = _On(dev, stream)
-    try:
-        if out is None:
-            out = torch.empty((T, N), dtype=bf16, device=dev)
-        _check(lib().adafuse_gated_project(x.data_ptr(), T, K, ldx, W_gate.data_ptr(), W_up.data_ptr(), N, ldw, bg,
-                                           bu, out.data_ptr(), ldy, flags, s, on.raw), "adafuse_gated_project")
-    finally:
-        on.done()
-    return out
+    raw, ctx = _on(dev, stream)
+    return _call("adafuse_gated_project", ctx, (T, N), bf16, dev, out, lambda y: lib().adafuse_gated_project(
+        x.data_ptr(), T, K, ldx, W_gate.data_ptr(), W_up.data_ptr(), N, ldw, bg, bu, y, ldy, flags, s, raw))
 
 
 def epilogue(y, bias=None, activation=None, up=None, residual=None, out=None, out_dtype=None, stream=None):
@@ -328,27 +312,23 @@ def epilogue(y, bias=None, activation=None, up=None, residual=None, out=None, ou
     may be strided, those of y, up and residual one expanded row.  Returns
     `out`, bf16 [T, n] (or fp32); it may be y, up or residual itself."""
     import torch
-    bf16, f32 = torch.bfloat16, torch.float32
-    dev = y.device
-    ldy = _rows("y", y, (bf16, f32))
-    T, n = y.shape
-    kind = out.dtype if out is not None else out_dtype or bf16
-    if kind not in (bf16, f32) or (out_dtype is not None and kind != out_dtype):
-        raise ValueError("the result is bfloat16 or float32")
-    b = _vector("bias", bias, bf16, n, dev)
-    ldu = 0 if up is None else _rows("up", up, (y.dtype,), (T, n), dev)
-    ldr = 0 if residual is None else _rows("residual", residual, (bf16,), (T, n), dev)
-    ldo = n if out is None else _rows("out", out, (kind,), (T, n), dev)
-    flags = _activation(activation) | (IN_F32 if y.dtype is f32 else 0) | (OUT_F32 if kind is f32 else 0)
-    on = _On(dev, stream)
-    try:
-        if out is None:
-            out = torch.empty((T, n), dtype=kind, device=dev)
-        _check(lib().adafuse_epilogue(y.data_ptr(), T, n, ldy, b, _ptr(up), ldu, _ptr(residual), ldr, out.data_ptr(),
-                                      ldo, flags, on.raw), "adafuse_epilogue")
-    finally:
-        on.done()
-    return out
+    bf16, f32, dev = torch.bfloat16, torch.float32, y.get_device()
+    T, n = shape = _matrix("y", y)
+    given = f32 if y.dtype is f32 else bf16
+    ldy = _rows("y", y, given, shape, dev)
+    kind = bf16 if out is None and out_dtype is None else _result_type(out, out_dtype)
+    b = None if bias is None else _vector("bias", bias, bf16, n, dev)
+    u = r = None
+    ldu = ldr = 0
+    if up is not None:
+        u, ldu = up.data_ptr(), _rows("up", up, given, shape, dev)
+    if residual is not None:
+        r, ldr = residual.data_ptr(), _rows("residual", residual, bf16, shape, dev)
+    ldo = n if out is None else _rows("out", out, kind, shape, dev)
+    flags = _activation(activation) | (IN_F32 if given is f32 else 0) | (OUT_F32 if kind is f32 else 0)
+    raw, ctx = _on(dev, stream)
+    return _call("adafuse_epilogue", ctx, shape, kind, dev, out, lambda o: lib().adafuse_epilogue(
+        y.data_ptr(), T, n, ldy, b, u, ldu, r, ldr, o, ldo, flags, raw))
 
 
 def rotary_frequencies(dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
@@ -393,19 +373,22 @@ def rotary_frequencies(dim: int, base: float = 10000.0, scaling: Optional[str] =
     return freq.to(device) if device is not None else freq, mult
 
 
-def _heads(name: str, t, out, weight, D, T, dev):
+_HEADS = struct.Struct("@PPqqqqPi4x")       # adafuse_heads
+
+
+def _heads(name: str, t, out, weight, shape, dev: int) -> bytes:
     import torch
     bf16 = torch.bfloat16
-    for what, m in ((name, t), (name + "_out", out)):
-        if m.dtype != bf16 or m.dim() != 3 or m.shape[0] != T or m.shape[2] != D or m.shape[1] != t.shape[1]:
-            raise ValueError(f"{what}: expected bfloat16 [{T}, heads, {D}], got {m.dtype} {tuple(m.shape)}")
-        if m.stride(2) != 1 and D > 1:
-            raise ValueError(f"{what}: the elements of a head must be adjacent (strides {m.stride()})")
-        if m.device != dev:
-            raise ValueError(f"{what} is on {m.device}, not {dev}")
-    a, b = t.stride(), out.stride()
-    return Heads(t.data_ptr(), out.data_ptr(), a[0], a[1], b[0], b[1],
-                 _vector(name + "_weight", weight, bf16, D, dev), t.shape[1])
+    if t.dtype is not bf16 or out.dtype is not bf16 or t.shape != shape or out.shape != shape or \
+            t.get_device() != dev or out.get_device() != dev:
+        raise ValueError(f"{name}, {name}_out: expected {bf16} {tuple(shape)} on the call's device, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device} and {out.dtype} {tuple(out.shape)} on {out.device}")
+    its, ihs, i1 = t.stride()
+    ots, ohs, o1 = out.stride()
+    if (i1 != 1 or o1 != 1) and shape[2] > 1:
+        raise ValueError(f"{name}: the elements of a head must be adjacent (strides {t.stride()}, {out.stride()})")
+    w = 0 if weight is None else _vector(name + "_weight", weight, bf16, shape[2], dev)
+    return _HEADS.pack(t.data_ptr(), out.data_ptr(), its, ihs, ots, ohs, w, shape[1])
 
 
 def rotary(q, k, positions, freq, layout: str = "half", factor: float = 1.0, q_weight=None, k_weight=None,
@@ -419,34 +402,43 @@ def rotary(q, k, positions, freq, layout: str = "half", factor: float = 1.0, q_w
     elements.  q_weight / k_weight bf16 [D].  Returns (q_out, k_out), new
     contiguous tensors unless given; q_out may be q itself, k_out k."""
     import torch
-    dev = q.device
+    dev = q.get_device()
     if q.dim() != 3 or (k is not None and k.dim() != 3):
         raise ValueError("q and k have three dimensions: tokens, heads, elements")
-    T, _, D = q.shape
-    if layout not in ("half", "interleaved"):
-        raise ValueError(f"layout {layout!r} is neither 'half' nor 'interleaved'")
-    if positions.dtype not in (torch.int64, torch.int32) or tuple(positions.shape) != (T,) or \
-            (T > 1 and positions.stride(0) != 1) or positions.device != dev:
-        raise ValueError(f"positions: expected {T} adjacent int64 or int32 on {dev}")
+    T, Hq, D = shape = q.shape
+    flags = 0
+    if layout != "half":
+        if layout != "interleaved":
+            raise ValueError(f"layout {layout!r} is neither 'half' nor 'interleaved'")
+        flags = PAIRS
+    kind = torch.int64
+    if positions.dtype is torch.int32:
+        kind = torch.int32
+        flags |= POS_I32
+    p = _vector("positions", positions, kind, T, dev)
     if freq.dim() != 1:
         raise ValueError("freq has one dimension")
-    f = _vector("freq", freq, torch.float64, freq.shape[0], dev)
+    n = freq.shape[0]
+    f = _vector("freq", freq, torch.float64, n, dev)
     if k is None and (k_weight is not None or k_out is not None):
         raise ValueError("k_weight and k_out go with k")
-    flags = (PAIRS if layout == "interleaved" else 0) | (POS_I32 if positions.dtype is torch.int32 else 0)
-    on = _On(dev, stream)
-    try:
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        if k is not None and k_out is None:
+    raw, ctx = _on(dev, stream)
+    if ctx is not None:
+        with ctx:
+            if q_out is None:
+                q_out = torch.empty(shape, dtype=q.dtype, device=dev)
+            if k is not None and k_out is None:
+                k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+            return rotary(q, k, positions, freq, layout, factor, q_weight, k_weight, eps, q_out, k_out)
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=q.dtype, device=dev)
+    hk = None
+    if k is not None:
+        if k_out is None:
             k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-        hq = _heads("q", q, q_out, q_weight, D, T, dev)
-        hk = None if k is None else _heads("k", k, k_out, k_weight, D, T, dev)
-        _check(lib().adafuse_rotary(ctypes.byref(hq), None if hk is None else ctypes.byref(hk), T, D,
-                                    2 * freq.shape[0], positions.data_ptr(), f, factor, eps, flags, on.raw),
-               "adafuse_rotary")
-    finally:
-        on.done()
+        hk = _heads("k", k, k_out, k_weight, (T, k.shape[1], D), dev)
+    _check(lib().adafuse_rotary(_heads("q", q, q_out, q_weight, shape, dev), hk, T, D, 2 * n, p, f, factor, eps,
+                                flags, raw), "adafuse_rotary")
     return q_out, k_out
 
 

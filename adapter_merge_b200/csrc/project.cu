@@ -30,30 +30,34 @@
 
 #include "act.cuh"
 #include "internal.h"
+#include "project.h"
 #include "ptx.cuh"
 
 namespace af {
+
+bool encode_rows(CUtensorMap* m, const void* p, int64_t rows, int32_t cols, int64_t ld, int box_rows)
+{
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)(rows > 1 ? ld : cols) * 2};
+    cuuint32_t box[2] = {kChunkK, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box,
+                                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 constexpr int kStreamThreads = 192;                     // producer, MMA, four epilogue warps
 constexpr int kMaxRing = 12;
 constexpr int kMaxSplits = 8;
 constexpr uint32_t kWTile = kTileM * kChunkK * 2;       // 16 KB
-constexpr int kPartCols = 512;                          // columns per accumulator of an fp32 output
 
-struct StreamArgs {
-    void* y;
-    const uint16_t* residual;
-    const uint16_t* bias;
-    const uint16_t* bias_up;
-    int32_t* status;
-    int64_t ldy, ldr, T;
-    int32_t N;              // d_out
+struct StreamArgs : ProjectArgs {
     int32_t tile;           // tokens per unit: a multiple of 16
     int32_t n_tt;           // token tiles
-    int32_t chunks, splits, ring, parts;
-    uint32_t tmem_cols, stage_bytes, act;
-    int32_t y_f32, stall;
+    int32_t splits, ring, parts;
+    uint32_t tmem_cols, stage_bytes;
 };
 
 // bias, activation, product and residual of 8 consecutive outputs, and their store
@@ -259,18 +263,6 @@ __global__ void __launch_bounds__(kStreamThreads) stream_kernel(const __grid_con
 
 // ------------------------------------------------------------------ host side
 
-// bf16 [rows, cols] with rows `ld` elements apart, boxes of 64 columns x box_rows, 128-byte swizzle
-bool encode_rows(CUtensorMap* m, const void* p, int64_t rows, int32_t cols, int64_t ld, int box_rows)
-{
-    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)(rows > 1 ? ld : cols) * 2};
-    cuuint32_t box[2] = {kChunkK, (cuuint32_t)box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box,
-                                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Shared memory per CTA of the two ways to run the stream kernel: two CTAs on
 // an SM, or one.
 constexpr uint32_t kSmemHalf = 111 * 1024, kSmemFull = 225 * 1024;
@@ -301,21 +293,12 @@ int clusters_at_once(int dev, int splits, bool half)
     return v;
 }
 
-struct Call {
-    const void *x, *W, *W_up;
-    int64_t ldx, ldw;
-    int32_t K;
-    StreamArgs a;
-    cudaStream_t s;
-};
-
 template <bool kGated>
-int launch_stream(Call& c)
+int launch_stream(ProjectCall& c)
 {
-    StreamArgs& a = c.a;
+    StreamArgs a{c.a};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return ADAFUSE_ERR_DEVICE;
-    a.chunks = (c.K + kChunkK - 1) / kChunkK;
     // the fewest token tiles, of equal height
     const int most = kGated ? 128 : 256;
     a.n_tt = (int)((a.T + most - 1) / most);
@@ -359,9 +342,19 @@ int launch_stream(Call& c)
                               half ? kSmemHalf : kSmemFull, a.splits, c.s, xm, wm, um, a);
 }
 
-int check(Call& c, const void* bias, const void* bias_up, bool gated, uint32_t flags)
+// Up to this many tokens W streams past them; above, tiles of tokens and
+// outputs on CTA pairs.
+constexpr int64_t kStreamTokens = 256;
+
+template <bool kGated>
+int launch_project(ProjectCall& c)
 {
-    StreamArgs& a = c.a;
+    return c.a.T <= kStreamTokens ? launch_stream<kGated>(c) : launch_project_tile(c);
+}
+
+int check(ProjectCall& c, const void* bias, const void* bias_up, bool gated, uint32_t flags)
+{
+    ProjectArgs& a = c.a;
     const uint32_t act = flags & ADAFUSE_ACT_MASK;
     if (flags & ~(ADAFUSE_ACT_MASK | ADAFUSE_TEST_STALL | (gated ? 0u : ADAFUSE_OUT_F32))) return ADAFUSE_ERR_INVALID_ARG;
     if (a.T < 0 || c.K < 1 || a.N < 1) return ADAFUSE_ERR_INVALID_ARG;
@@ -389,6 +382,7 @@ int check(Call& c, const void* bias, const void* bias_up, bool gated, uint32_t f
     a.bias = static_cast<const uint16_t*>(bias);
     a.bias_up = static_cast<const uint16_t*>(bias_up);
     a.act = act;
+    a.chunks = (c.K + kChunkK - 1) / kChunkK;
     a.stall = flags & ADAFUSE_TEST_STALL ? 1 : 0;
     if (!device_sms()) return ADAFUSE_ERR_DEVICE;
     if (!tensor_map_encoder()) return ADAFUSE_ERR_CUDA;
@@ -405,7 +399,7 @@ extern "C" int adafuse_project(const void* x, int64_t T, int32_t d_in, int64_t x
                                int64_t r_row_stride, void* y, int64_t y_row_stride, uint32_t flags, int32_t* status,
                                adafuse_stream_t stream)
 {
-    Call c{x, W, nullptr, x_row_stride, w_row_stride, d_in, {}, (cudaStream_t)stream};
+    ProjectCall c{x, W, nullptr, x_row_stride, w_row_stride, d_in, {}, (cudaStream_t)stream};
     c.a.y = y;
     c.a.residual = static_cast<const uint16_t*>(residual);
     c.a.ldy = y_row_stride;
@@ -415,7 +409,7 @@ extern "C" int adafuse_project(const void* x, int64_t T, int32_t d_in, int64_t x
     c.a.status = status;
     const int rc = check(c, bias, nullptr, false, flags);
     if (rc || T == 0) return rc;
-    return launch_stream<false>(c);
+    return launch_project<false>(c);
 }
 
 extern "C" int adafuse_gated_project(const void* x, int64_t T, int32_t d_in, int64_t x_row_stride,
@@ -423,7 +417,7 @@ extern "C" int adafuse_gated_project(const void* x, int64_t T, int32_t d_in, int
                                      const void* bias_gate, const void* bias_up, void* y, int64_t y_row_stride,
                                      uint32_t flags, int32_t* status, adafuse_stream_t stream)
 {
-    Call c{x, W_gate, W_up, x_row_stride, w_row_stride, d_in, {}, (cudaStream_t)stream};
+    ProjectCall c{x, W_gate, W_up, x_row_stride, w_row_stride, d_in, {}, (cudaStream_t)stream};
     c.a.y = y;
     c.a.ldy = y_row_stride;
     c.a.T = T;
@@ -431,5 +425,5 @@ extern "C" int adafuse_gated_project(const void* x, int64_t T, int32_t d_in, int
     c.a.status = status;
     const int rc = check(c, bias_gate, bias_up, true, flags);
     if (rc || T == 0) return rc;
-    return launch_stream<true>(c);
+    return launch_project<true>(c);
 }

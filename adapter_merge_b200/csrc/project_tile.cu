@@ -1,0 +1,422 @@
+// The projections of project.cu for many tokens: compute-bound, on CTA pairs.
+//
+// A tile is 256 tokens x 256 (or 128) accumulator columns, computed by a pair
+// of CTAs with cta_group::2 products: each CTA loads its half of the tokens
+// and its half of the W rows (for the gated form one CTA loads gate rows, the
+// other the up rows of the same outputs, so the two halves of a tile's columns
+// are act's argument and its factor), and holds the accumulator of its own 128
+// tokens in TMEM, twice, so the epilogue of one tile runs under the products
+// of the next.  One warp per CTA loads by TMA into a ring, one thread of the
+// pair issues the products, eight warps of each CTA read the accumulator, add
+// the bias, the activation, the factor and the residual in fp32, round, and
+// turn the rows through shared memory so that every store writes whole
+// sectors.  The pairs are persistent and walk the tiles in groups of eight
+// token tiles, so that the tiles in flight share both operands in L2.
+//
+// fp32 outputs take a fresh accumulator every 512 columns of d_in, added up in
+// the epilogue's registers (the tensor core's rounding towards zero adds up
+// over long sums, see project.cu).
+#include <algorithm>
+#include <atomic>
+
+#include "act.cuh"
+#include "project.h"
+#include "ptx.cuh"
+
+namespace af {
+namespace {
+
+constexpr int kTileThreads = 320;               // producer, MMA, eight epilogue warps
+constexpr int kEpiWarps = 8;
+constexpr int kPairTokens = 256;
+constexpr int kGroup = 8;                       // token tiles per group of the walk
+constexpr uint32_t kTileSmem = 226 * 1024;      // the whole SM: no other tcgen05 kernel beside a pair
+constexpr uint32_t kRowPitch = 80;              // 64 bytes of a row and 16 of padding
+constexpr uint32_t kTurnBytes = kEpiWarps * 32 * kRowPitch;
+constexpr uint32_t kXBytes = 128 * kChunkK * 2; // a CTA's tokens of a chunk
+
+template <int kCols>
+struct Ring {
+    static constexpr uint32_t kWBytes = kCols / 2 * kChunkK * 2;
+    static constexpr uint32_t kStage = kXBytes + kWBytes;
+    static constexpr int kStages = (int)((kTileSmem - 1024 - kTurnBytes) / kStage);
+};
+
+struct TileArgs : ProjectArgs {
+    int32_t m_tiles, n_tiles, out_cols;         // outputs per tile
+    int32_t part;                               // chunks per accumulator
+    int64_t tiles;
+};
+
+template <int N>
+__device__ __forceinline__ void activate_all(float (&v)[N], uint32_t act)
+{
+    switch (act) {
+        case ADAFUSE_ACT_NONE: return;
+        case ADAFUSE_ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = activate(v[i], ADAFUSE_ACT_RELU);
+            return;
+        case ADAFUSE_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = activate(v[i], ADAFUSE_ACT_SILU);
+            return;
+        case ADAFUSE_ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = activate(v[i], ADAFUSE_ACT_GELU);
+            return;
+        default:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = activate(v[i], ADAFUSE_ACT_GELU_TANH);
+            return;
+    }
+}
+
+// Adds p[0 .. N) (bf16, 16-byte aligned) to v; groups of 8 from `limit` on are not read.
+template <int N>
+__device__ __forceinline__ void add_bf16(float (&v)[N], const uint16_t* p, int limit)
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+        if (i < limit) {
+            const uint4 w = *reinterpret_cast<const uint4*>(p + i);
+            v[i] += bf16lo(w.x); v[i + 1] += bf16hi(w.x); v[i + 2] += bf16lo(w.y); v[i + 3] += bf16hi(w.y);
+            v[i + 4] += bf16lo(w.z); v[i + 5] += bf16hi(w.z); v[i + 6] += bf16lo(w.w); v[i + 7] += bf16hi(w.w);
+        }
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void load_cols(uint32_t taddr, float (&v)[N])
+{
+    static_assert(N == 32, "one load");
+    uint32_t r[32];
+    tc_ld_x32(taddr, r);
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// A warp's 32 rows x 64 bytes, one row per lane as `w`, written to y with four
+// lanes per row.  `limit`: bytes of a row that y has.
+__device__ __forceinline__ void store_rows(uint8_t* turn, const uint4 (&w)[4], uint8_t* y, int64_t pitch, int64_t rows,
+                                           int limit)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(turn + lane * kRowPitch + i * 16) = w[i];
+    __syncwarp();
+    const int piece = (lane & 3) * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2);
+        const uint4 v = *reinterpret_cast<const uint4*>(turn + r * kRowPitch + piece);
+        if (r < rows && piece < limit) *reinterpret_cast<uint4*>(y + r * pitch + piece) = v;
+    }
+    __syncwarp();
+}
+
+__device__ __forceinline__ uint4 pack8(const float* v)
+{
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
+}
+
+// 32 finished columns (outputs o ..) of the warp's 32 tokens (t0 ..): bias and
+// activation are done by the caller where a factor follows them.
+template <bool kF32>
+__device__ __forceinline__ void finish32(const TileArgs& a, float (&v)[32], int64_t t0, int o, uint8_t* turn)
+{
+    const int lane = threadIdx.x & 31;
+    const int cols = a.N - o;           // outputs that exist from o on
+    const int64_t rows = a.T - t0;
+    if (a.residual && lane < rows) add_bf16(v, a.residual + (t0 + lane) * a.ldr + o, cols);
+    if constexpr (kF32) {
+        float* y = static_cast<float*>(a.y) + t0 * a.ldy + o;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint4 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = make_uint4(__float_as_uint(v[16 * h + 4 * i]), __float_as_uint(v[16 * h + 4 * i + 1]),
+                                  __float_as_uint(v[16 * h + 4 * i + 2]), __float_as_uint(v[16 * h + 4 * i + 3]));
+            store_rows(turn, w, reinterpret_cast<uint8_t*>(y + 16 * h), a.ldy * 4, rows, (cols - 16 * h) * 4);
+        }
+    } else {
+        uint16_t* y = static_cast<uint16_t*>(a.y) + t0 * a.ldy + o;
+        const uint4 w[4] = {pack8(v), pack8(v + 8), pack8(v + 16), pack8(v + 24)};
+        store_rows(turn, w, reinterpret_cast<uint8_t*>(y), a.ldy * 2, rows, cols * 2);
+    }
+}
+
+// kCols: accumulator columns of a tile.  kF32: fp32 outputs (never gated).
+template <int kCols, bool kGated, bool kF32>
+__global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_constant__ CUtensorMap xmap,
+                                                               const __grid_constant__ CUtensorMap wmap,
+                                                               const __grid_constant__ CUtensorMap umap,
+                                                               const TileArgs a)
+{
+    using R = Ring<kCols>;
+    constexpr int kStages = R::kStages;
+    extern __shared__ uint8_t dyn[];
+    __shared__ uint64_t full[kStages], empty[kStages], accfull[2], accempty[2], done;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
+    uint8_t* turns = ring + (size_t)kStages * R::kStage;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&accfull[i], 1);
+            mbar_init(&accempty[i], 2 * kEpiWarps);
+        }
+        mbar_init(&done, 1);
+        fence_mbar_init();
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    if (warp == 1) {
+        tmem_alloc_pair(&tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    // tile i of the walk: groups of kGroup token tiles, token tiles fastest
+    const auto tile_at = [&](int64_t i, int& m, int& n) {
+        const int64_t per = (int64_t)kGroup * a.n_tiles;
+        const int64_t g = i / per;
+        const int rows = min(kGroup, a.m_tiles - (int)g * kGroup);
+        const int64_t j = i - g * per;
+        m = (int)g * kGroup + (int)(j % rows);
+        n = (int)(j / rows);
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int64_t it = 0;             // chunks so far
+            bool stop = false;
+            for (int64_t i = pair; i < a.tiles && !stop; i += pairs) {
+                int m, n;
+                tile_at(i, m, n);
+                const int t = m * kPairTokens + rank * 128;
+                const int row = kGated ? n * a.out_cols : n * a.out_cols + rank * (kCols / 2);
+                const CUtensorMap* w = kGated && rank ? &umap : &wmap;
+                for (int c = 0; c < a.chunks; ++c, ++it) {
+                    const int s = (int)(it % kStages);
+                    if (it >= kStages && !mbar_wait(&empty[s], (uint32_t)(it / kStages - 1) & 1, &abort_flag)) {
+                        stop = true;
+                        break;
+                    }
+                    if (a.stall && blockIdx.x == 0 && it == 0) continue;        // test hook: never arrives
+                    uint8_t* p = ring + (size_t)s * R::kStage;
+                    const uint32_t bar = cluster_map(smem_u32(&full[s]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * R::kStage);
+                    tma_load_2d_pair(p, &xmap, bar, c * kChunkK, t);
+                    tma_load_2d_pair(p + kXBytes, w, bar, c * kChunkK, row);
+                }
+            }
+            // Every stage's last products have signalled before the CTA leaves;
+            // after an abort, what is in flight has landed.
+            const int64_t from = max((int64_t)0, it - kStages);
+            for (int64_t j = from; j < it && !abort_flag; ++j)
+                mbar_wait(&empty[j % kStages], (uint32_t)(j / kStages) & 1, &abort_flag);
+            if (abort_flag && rank == 0)
+                for (int64_t j = from; j < it; ++j)
+                    if (!(a.stall && blockIdx.x == 0 && j == 0))
+                        mbar_wait_landed(&full[j % kStages], (uint32_t)(j / kStages) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = make_idesc_bf16(256, kCols, 0u, 0u);
+            int64_t it = 0, use = 0;    // chunks and accumulators so far
+            bool stop = false;
+            for (int64_t i = pair; i < a.tiles && !stop; i += pairs) {
+                for (int c = 0; c < a.chunks; ++c, ++it) {
+                    const bool fresh = kF32 ? c % a.part == 0 : c == 0;
+                    if (fresh) {
+                        if (!mbar_wait(&accempty[use & 1], ((uint32_t)(use >> 1) & 1) ^ 1u, &abort_flag)) {
+                            stop = true;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
+                    const uint32_t d = tmem + (uint32_t)(use & 1) * kCols;
+                    const int s = (int)(it % kStages);
+                    if (!mbar_wait(&full[s], (uint32_t)(it / kStages) & 1, &abort_flag)) {
+                        stop = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t x = smem_u32(ring + (size_t)s * R::kStage), w = x + kXBytes;
+#pragma unroll
+                    for (int kk = 0; kk < kChunkK / 16; ++kk)
+                        tc_mma_bf16_pair(d, make_sdesc(x + kk * 32u, 16u, 1024u, kLayoutSw128),
+                                         make_sdesc(w + kk * 32u, 16u, 1024u, kLayoutSw128), idesc,
+                                         fresh && kk == 0 ? 0u : 1u);
+                    tc_commit_pair(&empty[s]);
+                    if (c == a.chunks - 1 || (kF32 && (c + 1) % a.part == 0)) {
+                        tc_commit_pair(&accfull[use & 1]);
+                        ++use;
+                    }
+                }
+            }
+            if (abort_flag) {
+                tc_commit_pair(&done);
+                mbar_wait_landed(&done, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        uint8_t* turn = turns + (warp - 2) * 32 * kRowPitch;
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+        const uint32_t free0 = cluster_map(smem_u32(&accempty[0]), 0), free1 = cluster_map(smem_u32(&accempty[1]), 0);
+        int64_t use = 0;
+        bool ok = true;
+        // waits for the next accumulator; gives it back
+        const auto take = [&]() {
+            ok = mbar_wait(&accfull[use & 1], (uint32_t)(use >> 1) & 1, &abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            return ok;
+        };
+        const auto give = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(use & 1 ? free1 : free0);
+            ++use;
+        };
+        for (int64_t i = pair; i < a.tiles; i += pairs) {
+            int m, n;
+            tile_at(i, m, n);
+            const int64_t t0 = (int64_t)m * kPairTokens + rank * 128 + q * 32;
+            if constexpr (kGated) {
+                constexpr int kMine = kCols / 4;            // outputs per warp
+                const int o0 = n * a.out_cols + half * kMine;
+                if (!take()) break;
+                const uint32_t d = lanes + (uint32_t)(use & 1) * kCols + half * kMine;
+#pragma unroll
+                for (int c = 0; c < kMine; c += 32) {
+                    float v[32], u[32];
+                    load_cols(d + c, v);
+                    load_cols(d + kCols / 2 + c, u);
+                    if (a.bias) add_bf16(v, a.bias + o0 + c, a.N - o0 - c);
+                    if (a.bias_up) add_bf16(u, a.bias_up + o0 + c, a.N - o0 - c);
+                    activate_all(v, a.act);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] *= u[j];
+                    finish32<false>(a, v, t0, o0 + c, turn);
+                }
+                give();
+            } else if constexpr (!kF32) {
+                constexpr int kMine = kCols / 2;
+                const int o0 = n * a.out_cols + half * kMine;
+                if (!take()) break;
+                const uint32_t d = lanes + (uint32_t)(use & 1) * kCols + half * kMine;
+#pragma unroll 1
+                for (int c = 0; c < kMine; c += 32) {
+                    float v[32];
+                    load_cols(d + c, v);
+                    if (a.bias) add_bf16(v, a.bias + o0 + c, a.N - o0 - c);
+                    activate_all(v, a.act);
+                    finish32<false>(a, v, t0, o0 + c, turn);
+                }
+                give();
+            } else {
+                constexpr int kMine = kCols / 2, kParts = kMine / 32;
+                const int o0 = n * a.out_cols + half * kMine;
+                float v[kParts][32];
+                for (int c0 = 0; c0 < a.chunks; c0 += a.part) {
+                    if (!take()) break;
+                    const uint32_t d = lanes + (uint32_t)(use & 1) * kCols + half * kMine;
+#pragma unroll
+                    for (int c = 0; c < kParts; ++c) {
+                        float p[32];
+                        load_cols(d + c * 32, p);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[c][j] = c0 ? v[c][j] + p[j] : p[j];
+                    }
+                    give();
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < kParts; ++c) {
+                    const int o = o0 + c * 32;
+                    if (a.bias) add_bf16(v[c], a.bias + o, a.N - o);
+                    activate_all(v[c], a.act);
+                    finish32<true>(a, v[c], t0, o, turn);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && *(volatile int*)&abort_flag && a.status) atomicOr(a.status, ADAFUSE_STATUS_TIMEOUT);
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+template <int kCols, bool kGated, bool kF32>
+int launch_tiles(ProjectCall& c, int pairs)
+{
+    TileArgs a{c.a};
+    a.out_cols = kGated ? kCols / 2 : kCols;
+    a.m_tiles = (int)((a.T + kPairTokens - 1) / kPairTokens);
+    a.n_tiles = (a.N + a.out_cols - 1) / a.out_cols;
+    a.tiles = (int64_t)a.m_tiles * a.n_tiles;
+    a.part = kPartCols / kChunkK;
+    auto kernel = tile_kernel<kCols, kGated, kF32>;
+    static std::atomic<uint64_t> ready{0};          // devices whose kernel may use all shared memory
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ADAFUSE_ERR_DEVICE;
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTileSmem) != cudaSuccess)
+            return ADAFUSE_ERR_CUDA;
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    CUtensorMap xm, wm, um;
+    if (!encode_rows(&xm, c.x, a.T, c.K, c.ldx, 128) || !encode_rows(&wm, c.W, a.N, c.K, c.ldw, kCols / 2))
+        return ADAFUSE_ERR_UNSUPPORTED;
+    if (!kGated) um = wm;
+    else if (!encode_rows(&um, c.W_up, a.N, c.K, c.ldw, kCols / 2)) return ADAFUSE_ERR_UNSUPPORTED;
+    const int64_t n = std::min<int64_t>(a.tiles, pairs);
+    return launch_pdl_cluster(kernel, dim3((unsigned)(2 * n)), dim3(kTileThreads), kTileSmem, 2, c.s, xm, wm, um, a);
+}
+
+}  // namespace
+
+int launch_project_tile(ProjectCall& c)
+{
+    const int pairs = device_sms() / 2;
+    const bool gated = c.W_up != nullptr;
+    if (c.a.T > 0x7fffffff - kPairTokens) return ADAFUSE_ERR_UNSUPPORTED;
+    // Wide tiles feed the tensor core best; narrow ones where the last round
+    // of wide tiles would leave many pairs idle.
+    const int64_t m = (c.a.T + kPairTokens - 1) / kPairTokens;
+    const auto rounds = [&](int cols) {
+        const int out = gated ? cols / 2 : cols;
+        return (m * ((c.a.N + out - 1) / out) + pairs - 1) / pairs;
+    };
+    const bool wide = 2 * rounds(256) <= rounds(128) + 0.1 * rounds(128);
+    if (gated) return wide ? launch_tiles<256, true, false>(c, pairs) : launch_tiles<128, true, false>(c, pairs);
+    // 64 sums per lane beside the epilogue's own values; 128 would not fit the registers
+    if (c.a.y_f32) return launch_tiles<128, false, true>(c, pairs);
+    return wide ? launch_tiles<256, false, false>(c, pairs) : launch_tiles<128, false, false>(c, pairs);
+}
+
+}  // namespace af
