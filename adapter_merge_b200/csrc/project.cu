@@ -133,54 +133,61 @@ __global__ void __launch_bounds__(kStreamThreads) stream_kernel(const __grid_con
     const uint32_t tmem = tmem_slot;
 
     if (warp == 0) {
-        if (lane == 0) {
-            int issued = 0;
-            for (int i = 0; i < n; ++i) {
-                const int s = i % a.ring;
-                if (i >= a.ring && !mbar_wait(&empty[s], (uint32_t)(i / a.ring - 1) & 1, &abort_flag)) break;
-                if (a.stall && blockIdx.x == 0 && i == 0) continue;         // test hook: never arrives
+        // The whole warp walks the loop, one elected lane issues the copies.
+        int s = 0, issued = 0;
+        uint32_t lap = 1;               // parity that the stage's `empty` completes with when free (the first lap: at once)
+        for (int i = 0; i < n; ++i) {
+            if (!mbar_wait_warp(&empty[s], lap, &abort_flag)) break;
+            if (!(a.stall && blockIdx.x == 0 && i == 0) && elect_one()) {       // test hook: the first never arrives
                 uint8_t* p = ring + (size_t)s * a.stage_bytes;
                 const int k = (c0 + i) * kChunkK;
                 mbar_arrive_expect_tx(&full[s], a.stage_bytes);
                 tma_load_2d(p, &wmap, &full[s], k, row0);
                 if constexpr (kGated) tma_load_2d(p + kWTile, &umap, &full[s], k, row0);
                 tma_load_2d(p + (kGated ? 2 : 1) * kWTile, &xmap, &full[s], k, (int)t0);
-                issued = i + 1;
             }
-            // a wait gave up: what is in flight has to land before shared memory is given back
-            if (abort_flag)
-                for (int i = max(0, issued - a.ring); i < issued; ++i)
-                    if (!(a.stall && blockIdx.x == 0 && i == 0))
-                        mbar_wait_landed(&full[i % a.ring], (uint32_t)(i / a.ring) & 1);
+            __syncwarp();
+            issued = i + 1;
+            if (++s == a.ring) { s = 0; lap ^= 1; }
         }
+        // a wait gave up: what is in flight has to land before shared memory is given back
+        if (__any_sync(0xffffffffu, *(volatile int*)&abort_flag))
+            for (int i = max(0, issued - a.ring); i < issued; ++i)
+                if (!(a.stall && blockIdx.x == 0 && i == 0))
+                    mbar_wait_landed(&full[i % a.ring], (uint32_t)(i / a.ring) & 1);
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = make_idesc_bf16(kTileM, (uint32_t)a.tile, 0u, 0u);
-            int part = -1;
-            for (int i = 0; i < n; ++i) {
-                const int s = i % a.ring;
-                if (!mbar_wait(&full[s], (uint32_t)(i / a.ring) & 1, &abort_flag)) break;
-                tc_fence_after();
-                const uint32_t w = smem_u32(ring + (size_t)s * a.stage_bytes);
-                const uint32_t x = w + (kGated ? 2 : 1) * kWTile;
-                const int now = (int)((int64_t)i * a.parts / n);
-                const bool fresh = now != part;
-                part = now;
+        const uint32_t idesc = make_idesc_bf16(kTileM, (uint32_t)a.tile, 0u, 0u);
+        const uint64_t desc = make_sdesc(smem_u32(ring), 16u, 1024u, kLayoutSw128);
+        const uint32_t xoff = ((kGated ? 2 : 1) * kWTile) >> 4;
+        int s = 0, part = 0, until = 0;         // the part that chunk i belongs to ends before chunk `until`
+        uint32_t lap = 0;
+        for (int i = 0; i < n; ++i) {
+            if (!mbar_wait_warp(&full[s], lap, &abort_flag)) break;
+            const bool fresh = i == until;
+            if (fresh) {
+                if (i) ++part;
+                until = (int)((int64_t)n * (part + 1) / a.parts);
+            }
+            if (elect_one()) {
+                const uint64_t w = desc + (uint64_t)(s * (int)(a.stage_bytes >> 4)), x = w + xoff;
                 const uint32_t d = tmem + (uint32_t)(part * a.tile);
 #pragma unroll
                 for (int kk = 0; kk < kChunkK / 16; ++kk) {
-                    const uint64_t bdesc = make_sdesc(x + kk * 32u, 16u, 1024u, kLayoutSw128);
                     const uint32_t acc = fresh && kk == 0 ? 0u : 1u;
-                    tc_mma_bf16(d, make_sdesc(w + kk * 32u, 16u, 1024u, kLayoutSw128), bdesc, idesc, acc);
+                    tc_mma_bf16(d, w + kk * 2, x + kk * 2, idesc, acc);
                     if constexpr (kGated)
-                        tc_mma_bf16(d + (uint32_t)a.tile, make_sdesc(w + kWTile + kk * 32u, 16u, 1024u, kLayoutSw128),
-                                    bdesc, idesc, acc);
+                        tc_mma_bf16(d + (uint32_t)a.tile, w + (kWTile >> 4) + kk * 2, x + kk * 2, idesc, acc);
                 }
                 tc_commit(&empty[s]);
+                if (i == n - 1) tc_commit(&done);
             }
-            tc_commit(&done);
-            if (abort_flag) mbar_wait_landed(&done, 0);
+            __syncwarp();
+            if (++s == a.ring) { s = 0; lap ^= 1; }
+        }
+        if (__any_sync(0xffffffffu, *(volatile int*)&abort_flag)) {
+            if (elect_one()) tc_commit(&done);
+            mbar_wait_landed(&done, 0);
         }
         __syncwarp();
     }
@@ -189,7 +196,7 @@ __global__ void __launch_bounds__(kStreamThreads) stream_kernel(const __grid_con
     // been consumed once the last product is done.
     float* part = reinterpret_cast<float*>(ring);
     if (warp >= 2) {
-        const bool ok = mbar_wait(&done, 0, &abort_flag) && !*(volatile int*)&abort_flag;
+        const bool ok = mbar_wait_hot(&done, 0, &abort_flag) && !*(volatile int*)&abort_flag;
         if (__all_sync(0xffffffffu, ok)) {
             tc_fence_after();
             const int q = warp & 3;

@@ -204,77 +204,89 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     };
 
     if (warp == 0) {
-        if (lane == 0) {
-            int64_t it = 0;             // chunks so far
-            bool stop = false;
-            for (int64_t i = pair; i < a.tiles && !stop; i += pairs) {
-                int m, n;
-                tile_at(i, m, n);
-                const int t = m * kPairTokens + rank * 128;
-                const int row = kGated ? n * a.out_cols : n * a.out_cols + rank * (kCols / 2);
-                const CUtensorMap* w = kGated && rank ? &umap : &wmap;
-                for (int c = 0; c < a.chunks; ++c, ++it) {
-                    const int s = (int)(it % kStages);
-                    if (it >= kStages && !mbar_wait(&empty[s], (uint32_t)(it / kStages - 1) & 1, &abort_flag)) {
-                        stop = true;
-                        break;
-                    }
-                    if (a.stall && blockIdx.x == 0 && it == 0) continue;        // test hook: never arrives
+        // The whole warp walks the loop and one elected lane issues the copies
+        // (and, below, the products: issued from a branch of one lane, with the
+        // others parked, a 64-column chunk of a 256 x 256 tile took 705 cycles
+        // instead of the 505 that its products take).
+        int64_t it = 0;             // chunks so far
+        int s = 0;                  // the ring's next stage
+        uint32_t lap = 1;           // parity that its `empty` completes with when free (the first lap: at once)
+        bool stop = false;
+        for (int64_t i = pair; i < a.tiles && !stop; i += pairs) {
+            int m, n;
+            tile_at(i, m, n);
+            const int t = m * kPairTokens + rank * 128;
+            const int row = kGated ? n * a.out_cols : n * a.out_cols + rank * (kCols / 2);
+            const CUtensorMap* w = kGated && rank ? &umap : &wmap;
+            for (int c = 0; c < a.chunks; ++c, ++it) {
+                if (!mbar_wait_warp(&empty[s], lap, &abort_flag)) {
+                    stop = true;
+                    break;
+                }
+                if (!(a.stall && blockIdx.x == 0 && it == 0) && elect_one()) {      // test hook: the first never arrives
                     uint8_t* p = ring + (size_t)s * R::kStage;
                     const uint32_t bar = cluster_map(smem_u32(&full[s]), 0);
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * R::kStage);
                     tma_load_2d_pair(p, &xmap, bar, c * kChunkK, t);
                     tma_load_2d_pair(p + kXBytes, w, bar, c * kChunkK, row);
                 }
+                __syncwarp();
+                if (++s == kStages) { s = 0; lap ^= 1; }
             }
-            // Every stage's last products have signalled before the CTA leaves;
-            // after an abort, what is in flight has landed.
-            const int64_t from = max((int64_t)0, it - kStages);
-            for (int64_t j = from; j < it && !abort_flag; ++j)
-                mbar_wait(&empty[j % kStages], (uint32_t)(j / kStages) & 1, &abort_flag);
-            if (abort_flag && rank == 0)
-                for (int64_t j = from; j < it; ++j)
-                    if (!(a.stall && blockIdx.x == 0 && j == 0))
-                        mbar_wait_landed(&full[j % kStages], (uint32_t)(j / kStages) & 1);
         }
+        // Every stage's last products have signalled before the CTA leaves;
+        // after an abort, what is in flight has landed.
+        const int64_t from = max((int64_t)0, it - kStages);
+        for (int64_t j = from; j < it; ++j)
+            if (!mbar_wait_warp(&empty[j % kStages], (uint32_t)(j / kStages) & 1, &abort_flag)) break;
+        if (rank == 0 && __any_sync(0xffffffffu, *(volatile int*)&abort_flag))
+            for (int64_t j = from; j < it; ++j)
+                if (!(a.stall && blockIdx.x == 0 && j == 0))
+                    mbar_wait_landed(&full[j % kStages], (uint32_t)(j / kStages) & 1);
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             constexpr uint32_t idesc = make_idesc_bf16(256, kCols, 0u, 0u);
-            int64_t it = 0, use = 0;    // chunks and accumulators so far
+            int s = 0;                  // the ring's next stage
+            uint32_t lap = 0;           // parity that its `full` completes with
+            uint32_t use = 0;           // accumulators so far
+            const uint64_t xdesc = make_sdesc(smem_u32(ring), 16u, 1024u, kLayoutSw128);
+            const uint64_t wdesc = make_sdesc(smem_u32(ring) + kXBytes, 16u, 1024u, kLayoutSw128);
             bool stop = false;
             for (int64_t i = pair; i < a.tiles && !stop; i += pairs) {
-                for (int c = 0; c < a.chunks; ++c, ++it) {
-                    const bool fresh = kF32 ? c % a.part == 0 : c == 0;
+                int left = 0;           // chunks until the next accumulator
+                for (int c = 0; c < a.chunks; ++c) {
+                    const bool fresh = left == 0;
                     if (fresh) {
-                        if (!mbar_wait(&accempty[use & 1], ((uint32_t)(use >> 1) & 1) ^ 1u, &abort_flag)) {
+                        if (!mbar_wait_warp(&accempty[use & 1], ((use >> 1) & 1) ^ 1u, &abort_flag)) {
                             stop = true;
                             break;
                         }
                         tc_fence_after();
+                        left = kF32 ? min(a.part, a.chunks - c) : a.chunks;
                     }
-                    const uint32_t d = tmem + (uint32_t)(use & 1) * kCols;
-                    const int s = (int)(it % kStages);
-                    if (!mbar_wait(&full[s], (uint32_t)(it / kStages) & 1, &abort_flag)) {
+                    if (!mbar_wait_warp(&full[s], lap, &abort_flag)) {
                         stop = true;
                         break;
                     }
-                    tc_fence_after();
-                    const uint32_t x = smem_u32(ring + (size_t)s * R::kStage), w = x + kXBytes;
+                    --left;
+                    if (elect_one()) {
+                        const uint32_t d = tmem + (use & 1) * kCols;
+                        const uint64_t at = (uint64_t)(s * (int)(R::kStage >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < kChunkK / 16; ++kk)
-                        tc_mma_bf16_pair(d, make_sdesc(x + kk * 32u, 16u, 1024u, kLayoutSw128),
-                                         make_sdesc(w + kk * 32u, 16u, 1024u, kLayoutSw128), idesc,
-                                         fresh && kk == 0 ? 0u : 1u);
-                    tc_commit_pair(&empty[s]);
-                    if (c == a.chunks - 1 || (kF32 && (c + 1) % a.part == 0)) {
-                        tc_commit_pair(&accfull[use & 1]);
-                        ++use;
+                        for (int kk = 0; kk < kChunkK / 16; ++kk)
+                            tc_mma_bf16_pair(d, xdesc + at + kk * 2, wdesc + at + kk * 2, idesc,
+                                             fresh && kk == 0 ? 0u : 1u);
+                        tc_commit_pair(&empty[s]);
+                        if (left == 0) tc_commit_pair(&accfull[use & 1]);
                     }
+                    __syncwarp();
+                    if (left == 0) ++use;
+                    if (++s == kStages) { s = 0; lap ^= 1; }
                 }
             }
-            if (abort_flag) {
-                tc_commit_pair(&done);
+            if (__any_sync(0xffffffffu, *(volatile int*)&abort_flag)) {
+                if (elect_one()) tc_commit_pair(&done);
                 mbar_wait_landed(&done, 0);
             }
         }
@@ -284,12 +296,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         uint8_t* turn = turns + (warp - 2) * 32 * kRowPitch;
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
         const uint32_t free0 = cluster_map(smem_u32(&accempty[0]), 0), free1 = cluster_map(smem_u32(&accempty[1]), 0);
-        int64_t use = 0;
+        uint32_t use = 0;
         bool ok = true;
         // waits for the next accumulator; gives it back
         const auto take = [&]() {
-            ok = mbar_wait(&accfull[use & 1], (uint32_t)(use >> 1) & 1, &abort_flag);
-            ok = __all_sync(0xffffffffu, ok);
+            ok = mbar_wait_warp(&accfull[use & 1], (use >> 1) & 1, &abort_flag);
             tc_fence_after();
             return ok;
         };
@@ -412,7 +423,7 @@ int launch_project_tile(ProjectCall& c)
         const int out = gated ? cols / 2 : cols;
         return (m * ((c.a.N + out - 1) / out) + pairs - 1) / pairs;
     };
-    const bool wide = 2 * rounds(256) <= rounds(128) + 0.1 * rounds(128);
+    const bool wide = rounds(256) <= 0.68 * rounds(128);
     if (gated) return wide ? launch_tiles<256, true, false>(c, pairs) : launch_tiles<128, true, false>(c, pairs);
     // 64 sums per lane beside the epilogue's own values; 128 would not fit the registers
     if (c.a.y_f32) return launch_tiles<128, false, true>(c, pairs);

@@ -96,6 +96,30 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
+// As mbar_wait, for waits that come every few hundred cycles: the clock and
+// the abort flag are looked at only after a run of tries.
+__device__ __forceinline__ bool mbar_wait_hot(uint64_t* bar, uint32_t parity, volatile int* abort)
+{
+    uint64_t t0 = 0;
+    while (true) {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        const uint64_t now = globaltimer_ns();
+        if (!t0) t0 = now;
+        if (now - t0 > kWaitLimitNs) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
+// The same by a whole converged warp, with one answer for all lanes.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort)
+{
+    return __all_sync(0xffffffffu, mbar_wait_hot(bar, parity, abort));
+}
+
 // As mbar_wait, but for copies and tensor-core work already in flight, which
 // have to land before the CTA may leave: goes on when *abort is raised.
 __device__ __forceinline__ bool mbar_wait_landed(uint64_t* bar, uint32_t parity)
@@ -130,6 +154,16 @@ __device__ __forceinline__ int ld_acquire_gpu(const int* p)
     int v;
     asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "elect.sync _|p, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(p) :: "memory");
+    return p != 0;
 }
 
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads)
