@@ -246,15 +246,16 @@ def _on(dev: int, stream):
                                   else torch.cuda.default_stream(device))
 
 
-def _call(name: str, ctx, shape, kind, dev: int, out, args):
-    """One library call: args(out, raw pointer of out); allocates `out` if None."""
-    import torch
+def _call(name: str, ctx, like, T: int, n: int, kind, out, args):
+    """One library call, args(pointer of out); allocates `out` [T, n] beside `like` if None."""
     if ctx is not None:
         with ctx:
-            return _call(name, None, shape, kind, dev, out, args)
+            return _call(name, None, like, T, n, kind, out, args)
     if out is None:
-        out = torch.empty(shape, dtype=kind, device=dev)
-    _check(args(out.data_ptr()), name)
+        out = like.new_empty(T, n) if like.dtype is kind else like.new_empty(T, n, dtype=kind)
+    rc = args(out.data_ptr())
+    if rc:
+        _check(rc, name)
     return out
 
 
@@ -280,7 +281,7 @@ def project(x, W, bias=None, activation=None, residual=None, out=None, out_dtype
     s = None if status is None else _vector("status", status, torch.int32, 1, dev)
     flags = _activation(activation) | (0 if kind is bf16 else OUT_F32)
     raw, ctx = _on(dev, stream)
-    return _call("adafuse_project", ctx, (T, N), kind, dev, out, lambda y: lib().adafuse_project(
+    return _call("adafuse_project", ctx, x, T, N, kind, out, lambda y: lib().adafuse_project(
         x.data_ptr(), T, K, ldx, W.data_ptr(), N, ldw, b, r, ldr or 0, y, N if ldy is None else ldy, flags, s, raw))
 
 
@@ -300,7 +301,7 @@ def gated_project(x, W_gate, W_up, bias_gate=None, bias_up=None, activation="sil
     s = None if status is None else _vector("status", status, torch.int32, 1, dev)
     flags = _activation(activation)
     raw, ctx = _on(dev, stream)
-    return _call("adafuse_gated_project", ctx, (T, N), bf16, dev, out, lambda y: lib().adafuse_gated_project(
+    return _call("adafuse_gated_project", ctx, x, T, N, bf16, out, lambda y: lib().adafuse_gated_project(
         x.data_ptr(), T, K, ldx, W_gate.data_ptr(), W_up.data_ptr(), N, ldw, bg, bu, y, ldy, flags, s, raw))
 
 
@@ -327,7 +328,7 @@ def epilogue(y, bias=None, activation=None, up=None, residual=None, out=None, ou
     ldo = n if out is None else _rows("out", out, kind, shape, dev)
     flags = _activation(activation) | (IN_F32 if given is f32 else 0) | (OUT_F32 if kind is f32 else 0)
     raw, ctx = _on(dev, stream)
-    return _call("adafuse_epilogue", ctx, shape, kind, dev, out, lambda o: lib().adafuse_epilogue(
+    return _call("adafuse_epilogue", ctx, y, T, n, kind, out, lambda o: lib().adafuse_epilogue(
         y.data_ptr(), T, n, ldy, b, u, ldu, r, ldr, o, ldo, flags, raw))
 
 
@@ -425,20 +426,19 @@ def rotary(q, k, positions, freq, layout: str = "half", factor: float = 1.0, q_w
     raw, ctx = _on(dev, stream)
     if ctx is not None:
         with ctx:
-            if q_out is None:
-                q_out = torch.empty(shape, dtype=q.dtype, device=dev)
-            if k is not None and k_out is None:
-                k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
             return rotary(q, k, positions, freq, layout, factor, q_weight, k_weight, eps, q_out, k_out)
     if q_out is None:
-        q_out = torch.empty(shape, dtype=q.dtype, device=dev)
+        q_out = q.new_empty(T, Hq, D)
     hk = None
     if k is not None:
+        Hk = k.shape[1]
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-        hk = _heads("k", k, k_out, k_weight, (T, k.shape[1], D), dev)
-    _check(lib().adafuse_rotary(_heads("q", q, q_out, q_weight, shape, dev), hk, T, D, 2 * n, p, f, factor, eps,
-                                flags, raw), "adafuse_rotary")
+            k_out = k.new_empty(T, Hk, D)
+        hk = _heads("k", k, k_out, k_weight, (T, Hk, D), dev)
+    rc = lib().adafuse_rotary(_heads("q", q, q_out, q_weight, shape, dev), hk, T, D, 2 * n, p, f, factor, eps,
+                              flags, raw)
+    if rc:
+        _check(rc, "adafuse_rotary")
     return q_out, k_out
 
 

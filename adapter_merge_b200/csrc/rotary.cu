@@ -10,12 +10,14 @@
 // The fraction goes to sincospif.
 //
 // HBM-bound for long prompts (each element read and written once), latency
-// for a decode batch.  A CTA takes a few tokens, computes their sines and
-// cosines once into shared memory (rot/2 per token, shared by all heads), then
-// its lanes rotate the heads: an item is a vector of V elements together with
-// the vector of its partners (one vector that holds both in the interleaved
-// layout, one unrotated vector past `rot`), and 2^n lanes share a head, one
-// item each, so that the norm's sum is a shuffle among them.
+// for a decode batch.  One warp, or several, take a token: each computes the
+// token's sines and cosines into shared memory (rot/2, shared by all heads; a
+// lane then keeps those of its own elements), then its lanes rotate the heads:
+// an item is a vector of V elements together with the vector of its partners
+// (one vector that holds both in the interleaved layout, one unrotated vector
+// past `rot`), and 2^n lanes share a head, one item each, so that the norm's
+// sum is a shuffle among them.  A lane loads the items of two heads (of four,
+// interleaved) before it rotates them.  No barrier across warps.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -24,7 +26,10 @@
 namespace af {
 namespace {
 
-constexpr int kRotThreads = 256;
+constexpr int kRotThreads = 128;
+constexpr int kRotWarps = kRotThreads / 32;
+constexpr int kFlight = 2;              // heads per lane in flight (four vectors)
+constexpr int kLaneHeads = 20;          // most heads of a prompt's token per lane
 constexpr int kMaxHeadDim = 1024;
 
 struct Heads {
@@ -43,26 +48,49 @@ struct RotArgs {
     int32_t D, rot, half;
     int32_t lanes;          // lanes per head: a power of two
     int32_t items;          // items per head
-    int32_t tokens;         // tokens per CTA
+    int32_t warps, warps_log2;      // warps per token: a power of two
     int32_t pairs, pos32;
     float factor, eps, inv_d;
+};
+
+// V bf16 elements as they come from memory.
+template <int V>
+struct Raw {
+    uint32_t w[V == 1 ? 1 : V / 2];
+    __device__ __forceinline__ void load(const uint16_t* p)
+    {
+        if constexpr (V == 8) {
+            const uint4 a = *reinterpret_cast<const uint4*>(p);
+            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        } else if constexpr (V == 4) {
+            const uint2 a = *reinterpret_cast<const uint2*>(p);
+            w[0] = a.x; w[1] = a.y;
+        } else {
+            w[0] = *p;
+        }
+    }
 };
 
 template <int V>
 struct Vec {
     float v[V];
+    __device__ __forceinline__ void from(const Raw<V>& r)
+    {
+        if constexpr (V == 1) {
+            v[0] = bf16lo(r.w[0]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                v[2 * i] = bf16lo(r.w[i]);
+                v[2 * i + 1] = bf16hi(r.w[i]);
+            }
+        }
+    }
     __device__ __forceinline__ void load(const uint16_t* p)
     {
-        if constexpr (V == 8) {
-            const uint4 a = *reinterpret_cast<const uint4*>(p);
-            v[0] = bf16lo(a.x); v[1] = bf16hi(a.x); v[2] = bf16lo(a.y); v[3] = bf16hi(a.y);
-            v[4] = bf16lo(a.z); v[5] = bf16hi(a.z); v[6] = bf16lo(a.w); v[7] = bf16hi(a.w);
-        } else if constexpr (V == 4) {
-            const uint2 a = *reinterpret_cast<const uint2*>(p);
-            v[0] = bf16lo(a.x); v[1] = bf16hi(a.x); v[2] = bf16lo(a.y); v[3] = bf16hi(a.y);
-        } else {
-            v[0] = __uint_as_float((uint32_t)*p << 16);
-        }
+        Raw<V> r;
+        r.load(p);
+        from(r);
     }
     __device__ __forceinline__ void store(uint16_t* p) const
     {
@@ -107,128 +135,200 @@ struct Item {
     }
 };
 
-template <int V>
-__device__ __forceinline__ void scale(Vec<V>& x, const uint16_t* w, float r)
+// The token's sines and cosines times the factor, by one warp.
+__device__ __forceinline__ void turn_token(const RotArgs& a, int64_t t, float* cosv, float* sinv)
 {
-    Vec<V> g;
-    g.load(w);
-#pragma unroll
-    for (int i = 0; i < V; ++i) x.v[i] = x.v[i] * r * g.v[i];
-}
-
-template <int V>
-__device__ __forceinline__ void rotate_item(const RotArgs& a, const Item<V>& it, const float2* cs, Vec<V>& x, Vec<V>& y)
-{
-    if (it.pair < 0) return;
-    if (it.o2 >= 0) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float2 c = cs[it.pair + i];
-            const float p = x.v[i], q = y.v[i];
-            x.v[i] = p * c.x - q * c.y;
-            y.v[i] = p * c.y + q * c.x;
-        }
-    } else if constexpr (V > 1) {
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            const float2 c = cs[it.pair + i];
-            const float p = x.v[2 * i], q = x.v[2 * i + 1];
-            x.v[2 * i] = p * c.x - q * c.y;
-            x.v[2 * i + 1] = p * c.y + q * c.x;
-        }
-    }
-}
-
-// kOne: a head has no more items than lanes, so its values stay in registers
-// between the norm's sum and the rotation; otherwise they are read again.
-template <int V, bool kOne>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotArgs a)
-{
-    extern __shared__ float2 cs[];          // [tokens][half]: cosine, sine, times the factor
-    griddep_wait();
-    griddep_launch_dependents();
-    const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
-    const int tokens = (int)min((int64_t)a.tokens, a.T - t0);
-    for (int i = threadIdx.x; i < tokens * a.half; i += kRotThreads) {
-        const int tl = i / a.half, f = i - tl * a.half;
-        const int64_t p = a.pos32 ? (int64_t)static_cast<const int32_t*>(a.pos)[t0 + tl]
-                                  : static_cast<const int64_t*>(a.pos)[t0 + tl];
+    if (!a.half) return;
+    const int64_t p = a.pos32 ? (int64_t)static_cast<const int32_t*>(a.pos)[t] : static_cast<const int64_t*>(a.pos)[t];
+    for (int f = threadIdx.x & 31; f < a.half; f += 32) {
         double turn = a.freq[f] * 0.15915494309189533577;       // 1 / (2 pi)
         turn -= floor(turn);
-        const uint64_t frac = __double2ull_rn(turn * 18446744073709551616.0);     // 2^64 itself wraps to 0 below
-        const int64_t at = (int64_t)((uint64_t)p * (turn < 1.0 ? frac : 0ull));
+        const uint64_t frac = turn < 1.0 ? __double2ull_rn(turn * 18446744073709551616.0) : 0ull;     // 2^64 turns
+        const int64_t at = (int64_t)((uint64_t)p * frac);
         float s, c;
         sincospif((float)at * 1.08420217248550443401e-19f, &s, &c);               // 2^-63 half turns
-        cs[i] = make_float2(c * a.factor, s * a.factor);
+        cosv[f] = c * a.factor;
+        sinv[f] = s * a.factor;
     }
-    __syncthreads();
+    __syncwarp();
+}
 
-    const int lane = threadIdx.x & (a.lanes - 1);
-    const int per = kRotThreads / a.lanes;          // heads at a time
-    const int tasks = tokens * a.H;
-    // Every lane of a warp takes the same number of steps (the shuffles need
-    // all of them); a step past the end does nothing.
-    for (int first = 0; first < tasks; first += per) {
-        const int task = first + (int)(threadIdx.x / a.lanes);
-        const bool live = task < tasks;
-        const int tl = live ? task / a.H : 0;
-        const int h = live ? task - tl * a.H : 0;
-        const bool is_q = h < a.Hq;
-        const Heads& m = is_q ? a.q : a.k;
-        const int hh = is_q ? h : h - a.Hq;
-        const uint16_t* in = m.in + (t0 + tl) * m.its + hh * m.ihs;
-        uint16_t* out = m.out + (t0 + tl) * m.ots + hh * m.ohs;
-        const float2* c = cs + tl * a.half;
-        Vec<V> x, y;
-        if constexpr (kOne) {
-            const Item<V> it(a, lane);
-            const bool mine = live && lane < a.items;
-            if (mine) {
-                x.load(in + it.o1);
-                if (it.o2 >= 0) y.load(in + it.o2);
+// The heads of one kind of a token, whose items (j of every head) one lane
+// holds: heads h0, h0 + stride, ...; the same number of steps for all lanes.
+// The coefficients of a pair (p, q) -> (p a - q b, p c + q d) hold the
+// weights, so a norm costs its sum and one factor more.
+template <int V, bool kPairs, bool kNorm>
+__device__ __forceinline__ void rotate_heads(const RotArgs& a, const Heads& m, int n, int64_t t, int h0, int stride,
+                                             int group, const Item<V>& it, bool mine, const float* cosv,
+                                             const float* sinv)
+{
+    constexpr int P = kPairs ? V / 2 : V;           // pairs of an item
+    constexpr int F = kPairs ? 2 * kFlight : kFlight;
+    const bool turns = it.pair >= 0, two = !kPairs && it.o2 >= 0;
+    float ca[P], cb[P], cc[P], cd[P];
+    if (mine) {
+        Vec<V> w0, w1;
+        if constexpr (kNorm) {
+            w0.load(m.weight + it.o1);
+            if (two) w1.load(m.weight + it.o2);
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float c = turns ? cosv[it.pair + i] : 1.f, s = turns ? sinv[it.pair + i] : 0.f;
+            const float wp = !kNorm ? 1.f : kPairs ? w0.v[2 * i] : w0.v[i];
+            const float wq = !kNorm ? 1.f : kPairs ? w0.v[2 * i + 1] : turns ? w1.v[i] : 0.f;
+            ca[i] = c * wp;
+            cb[i] = s * wq;
+            cc[i] = s * wp;
+            cd[i] = c * wq;
+        }
+    }
+    const uint16_t* in = m.in + t * m.its + h0 * m.ihs;
+    uint16_t* out = m.out + t * m.ots + h0 * m.ohs;
+    const int64_t din = stride * m.ihs, dout = stride * m.ohs;
+    for (int h = h0; h - group < n; h += F * stride) {
+        Raw<V> rx[F], ry[F];
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+            if (mine && h + j * stride < n) {
+                rx[j].load(in + it.o1);
+                if (two) ry[j].load(in + it.o2);
             }
-            if (a.q.weight || a.k.weight) {
-                float sum = mine ? x.squares() + (it.o2 >= 0 ? y.squares() : 0.f) : 0.f;
-                for (int d = a.lanes / 2; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                if (mine && m.weight) {
-                    const float r = rsqrtf(sum * a.inv_d + a.eps);
-                    scale<V>(x, m.weight + it.o1, r);
-                    if (it.o2 >= 0) scale<V>(y, m.weight + it.o2, r);
-                }
-            }
-            if (mine) {
-                rotate_item<V>(a, it, c, x, y);
-                x.store(out + it.o1);
-                if (it.o2 >= 0) y.store(out + it.o2);
-            }
-        } else {
+            in += din;
+        }
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+            const bool live = mine && h + j * stride < n;
+            Vec<V> x, y;
+            x.from(rx[j]);
+            if constexpr (!kPairs) y.from(ry[j]);
             float r = 1.f;
-            if (a.q.weight || a.k.weight) {
-                float sum = 0.f;
-                for (int j = lane; live && j < a.items; j += a.lanes) {
-                    const Item<V> it(a, j);
-                    x.load(in + it.o1);
-                    sum += x.squares();
-                    if (it.o2 >= 0) {
-                        y.load(in + it.o2);
-                        sum += y.squares();
-                    }
-                }
+            if constexpr (kNorm) {
+                float sum = live ? x.squares() : 0.f;
+                if (live && two) sum += y.squares();
                 for (int d = a.lanes / 2; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                 r = rsqrtf(sum * a.inv_d + a.eps);
             }
-            for (int j = lane; live && j < a.items; j += a.lanes) {
-                const Item<V> it(a, j);
-                x.load(in + it.o1);
-                if (it.o2 >= 0) y.load(in + it.o2);
-                if (m.weight) {
-                    scale<V>(x, m.weight + it.o1, r);
-                    if (it.o2 >= 0) scale<V>(y, m.weight + it.o2, r);
+            if (live) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    float& p = kPairs ? x.v[2 * i] : x.v[i];
+                    float& q = kPairs ? x.v[2 * i + 1] : y.v[i];
+                    if (turns) {
+                        const float u = p * ca[i] - q * cb[i];
+                        q = p * cc[i] + q * cd[i];
+                        p = u;
+                    } else if (kNorm) {
+                        p *= ca[i];
+                        if (kPairs) q *= cd[i];
+                    }
+                    if (kNorm) {
+                        p *= r;
+                        if (kPairs || two) q *= r;
+                    }
                 }
-                rotate_item<V>(a, it, c, x, y);
                 x.store(out + it.o1);
-                if (it.o2 >= 0) y.store(out + it.o2);
+                if constexpr (!kPairs)
+                    if (two) y.store(out + it.o2);
             }
+            out += dout;
+        }
+    }
+}
+
+// Heads of at most as many items as lanes share them.
+template <int V, bool kPairs, bool kNorm>
+__global__ void __launch_bounds__(kRotThreads, 5) rotary_kernel(const RotArgs a)
+{
+    extern __shared__ float angles[];       // per warp: rot/2 cosines, rot/2 sines
+    griddep_wait();
+    griddep_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t w = (int64_t)blockIdx.x * kRotWarps + warp, t = w >> a.warps_log2;
+    if (t >= a.T) return;
+    float* cosv = angles + warp * 2 * a.half;
+    float* sinv = cosv + a.half;
+    turn_token(a, t, cosv, sinv);
+    const int sub = lane & (a.lanes - 1), group = lane / a.lanes;
+    const int per = 32 / a.lanes, stride = per * a.warps;
+    const int first = ((int)w & (a.warps - 1)) * per + group;
+    const Item<V> it(a, sub);
+    const bool mine = sub < a.items;
+    if (kNorm && a.q.weight)
+        rotate_heads<V, kPairs, true>(a, a.q, a.Hq, t, first, stride, group, it, mine, cosv, sinv);
+    else
+        rotate_heads<V, kPairs, false>(a, a.q, a.Hq, t, first, stride, group, it, mine, cosv, sinv);
+    if (kNorm && a.k.weight)
+        rotate_heads<V, kPairs, true>(a, a.k, a.H - a.Hq, t, first, stride, group, it, mine, cosv, sinv);
+    else
+        rotate_heads<V, kPairs, false>(a, a.k, a.H - a.Hq, t, first, stride, group, it, mine, cosv, sinv);
+}
+
+// Any head: a warp walks its items, twice for a norm.
+template <int V>
+__global__ void __launch_bounds__(kRotThreads) rotary_any_kernel(const RotArgs a)
+{
+    extern __shared__ float angles[];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t w = (int64_t)blockIdx.x * kRotWarps + warp, t = w >> a.warps_log2;
+    if (t >= a.T) return;
+    float* cosv = angles + warp * 2 * a.half;
+    float* sinv = cosv + a.half;
+    turn_token(a, t, cosv, sinv);
+    const int sub = lane & (a.lanes - 1), group = lane / a.lanes;
+    const int per = 32 / a.lanes;
+    for (int h = ((int)w & (a.warps - 1)) * per + group; h - group < a.H; h += per * a.warps) {
+        const bool live = h < a.H;
+        const Heads& m = h < a.Hq ? a.q : a.k;
+        const int64_t hh = !live ? 0 : h < a.Hq ? h : h - a.Hq;
+        const uint16_t* in = m.in + t * m.its + hh * m.ihs;
+        uint16_t* out = m.out + t * m.ots + hh * m.ohs;
+        Vec<V> x, y, w;
+        float sum = 0.f;
+        for (int j = sub; live && m.weight && j < a.items; j += a.lanes) {
+            const Item<V> it(a, j);
+            x.load(in + it.o1);
+            sum += x.squares();
+            if (it.o2 >= 0) {
+                y.load(in + it.o2);
+                sum += y.squares();
+            }
+        }
+        for (int d = a.lanes / 2; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        const float r = rsqrtf(sum * a.inv_d + a.eps);
+        for (int j = sub; live && j < a.items; j += a.lanes) {
+            const Item<V> it(a, j);
+            x.load(in + it.o1);
+            if (it.o2 >= 0) y.load(in + it.o2);
+            if (m.weight) {
+                w.load(m.weight + it.o1);
+#pragma unroll
+                for (int i = 0; i < V; ++i) x.v[i] *= r * w.v[i];
+                if (it.o2 >= 0) {
+                    w.load(m.weight + it.o2);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) y.v[i] *= r * w.v[i];
+                }
+            }
+            if (it.o2 >= 0) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float c = cosv[it.pair + i], s = sinv[it.pair + i], p = x.v[i], q = y.v[i];
+                    x.v[i] = p * c - q * s;
+                    y.v[i] = p * s + q * c;
+                }
+            } else if (V > 1 && it.pair >= 0) {
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) {
+                    const float c = cosv[it.pair + i], s = sinv[it.pair + i], p = x.v[2 * i], q = x.v[2 * i + 1];
+                    x.v[2 * i] = p * c - q * s;
+                    x.v[2 * i + 1] = p * s + q * c;
+                }
+            }
+            x.store(out + it.o1);
+            if (it.o2 >= 0) y.store(out + it.o2);
         }
     }
 }
@@ -353,12 +453,26 @@ extern "C" int adafuse_rotary(const adafuse_heads* q, const adafuse_heads* k, in
     while (a.lanes < 32 && a.lanes < a.items) a.lanes *= 2;
     const int sms = device_sms();
     if (!sms) return ADAFUSE_ERR_DEVICE;
-    // Tokens per CTA: one while that leaves SMs without eight CTAs, up to four.
-    a.tokens = (int)std::max<int64_t>(1, std::min<int64_t>(4, T / ((int64_t)sms * 8)));
-    const int64_t blocks = (T + a.tokens - 1) / a.tokens;
+    // Warps per token: one while a lane has at most kLaneHeads heads (each
+    // warp computes the token's sines again: 4097 tokens of 80 heads took 32 us
+    // with 20 heads per lane, 41 us with five), but enough to give every SM
+    // its warps, as long as each has a head for its groups of lanes.
+    a.warps = 1;
+    while (a.warps * (32 / a.lanes) < a.H &&
+           (T * a.warps < (int64_t)sms * 16 || a.H > kLaneHeads * a.warps * (32 / a.lanes))) a.warps *= 2;
+    while ((1 << a.warps_log2) < a.warps) ++a.warps_log2;
+    const int64_t blocks = (T * a.warps + kRotWarps - 1) / kRotWarps;
     if (blocks > 0x7fffffff) return ADAFUSE_ERR_UNSUPPORTED;
-    auto kernel = V == 8 ? rotary_kernel<8, true> : one ? rotary_kernel<4, true>
-                : V == 4 ? rotary_kernel<4, false> : rotary_kernel<1, false>;
-    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kRotThreads), (size_t)a.tokens * a.half * sizeof(float2),
+    const bool norm = q->weight || (k && k->weight);
+    auto kernel = rotary_any_kernel<1>;
+    if (one && V == 8)
+        kernel = a.pairs ? (norm ? rotary_kernel<8, true, true> : rotary_kernel<8, true, false>)
+                         : (norm ? rotary_kernel<8, false, true> : rotary_kernel<8, false, false>);
+    else if (one)
+        kernel = a.pairs ? (norm ? rotary_kernel<4, true, true> : rotary_kernel<4, true, false>)
+                         : (norm ? rotary_kernel<4, false, true> : rotary_kernel<4, false, false>);
+    else if (V == 4)
+        kernel = rotary_any_kernel<4>;
+    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kRotThreads), (size_t)kRotWarps * rot * sizeof(float),
                       (cudaStream_t)stream, a);
 }
