@@ -95,10 +95,7 @@ __global__ void __launch_bounds__(kEpiThreads) epilogue_kernel(const EpiArgs a)
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] += w[i];
         }
-        if (a.act != ADAFUSE_ACT_NONE) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = activate(v[i], a.act);
-        }
+        activate_all(v, a.act);
         if (a.up) {
             load_group<V, kInF32>(a.up, row * a.ldu + c, w);
 #pragma unroll

@@ -10,7 +10,7 @@
 // and the tokens, padded to 16, as its N side, so that a single token costs
 // one pass over W.  A unit's d_in is split over the CTAs of a cluster: one
 // warp loads the CTA's range of 64-column chunks through a ring of shared
-// memory by TMA, one issues tcgen05.mma into TMEM, then the partial sums go
+// memory by TMA, two issue tcgen05.mma into TMEM, then the partial sums go
 // to shared memory (token by token), and each CTA adds up its share of the
 // tokens over the cluster's partials, always in rank order, applies the
 // epilogue and writes y.  No workspace, no counters, no atomics.  TMEM is
@@ -48,8 +48,8 @@ bool encode_rows(CUtensorMap* m, const void* p, int64_t rows, int32_t cols, int6
 
 namespace {
 
-constexpr int kStreamThreads = 192;                     // producer, MMA, four epilogue warps
-constexpr int kMaxRing = 12;
+constexpr int kStreamThreads = 256;                     // one warp loads, one multiplies; all finish
+constexpr int kMaxRing = 12;                            // stages of at least 18 KB
 constexpr int kMaxSplits = 8;
 constexpr uint32_t kWTile = kTileM * kChunkK * 2;       // 16 KB
 
@@ -70,10 +70,7 @@ __device__ __forceinline__ void finish8(const StreamArgs& a, float (&v)[8], floa
         d[4] += bf16lo(w.z); d[5] += bf16hi(w.z); d[6] += bf16lo(w.w); d[7] += bf16hi(w.w);
     };
     if (a.bias) add(v, a.bias + o);
-    if (a.act != ADAFUSE_ACT_NONE) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = activate(v[i], a.act);
-    }
+    activate_all(v, a.act);
     if constexpr (kGated) {
         if (a.bias_up) add(u, a.bias_up + o);
 #pragma unroll
@@ -92,8 +89,31 @@ __device__ __forceinline__ void finish8(const StreamArgs& a, float (&v)[8], floa
     }
 }
 
+// The 8 floats at this address in each CTA of the cluster, added in rank order.
+__device__ __forceinline__ void sum_partials(float (&v)[8], uint32_t at, int splits)
+{
+    float4 x[kMaxSplits][2];
+#pragma unroll
+    for (int r = 0; r < kMaxSplits; ++r) {
+        if (r < splits) {
+            const uint32_t p = splits > 1 ? cluster_map(at, (uint32_t)r) : at;
+            x[r][0] = ld_cluster_v4(p);
+            x[r][1] = ld_cluster_v4(p + 16);
+        } else {
+            x[r][0] = x[r][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+#pragma unroll
+    for (int r = 0; r < kMaxSplits; ++r) {
+        v[0] += x[r][0].x; v[1] += x[r][0].y; v[2] += x[r][0].z; v[3] += x[r][0].w;
+        v[4] += x[r][1].x; v[5] += x[r][1].y; v[6] += x[r][1].z; v[7] += x[r][1].w;
+    }
+}
+
 template <bool kGated>
-__global__ void __launch_bounds__(kStreamThreads) stream_kernel(const __grid_constant__ CUtensorMap xmap,
+__global__ void __launch_bounds__(kStreamThreads, 2) stream_kernel(const __grid_constant__ CUtensorMap xmap,
                                                                 const __grid_constant__ CUtensorMap wmap,
                                                                 const __grid_constant__ CUtensorMap umap,
                                                                 const StreamArgs a)
@@ -112,13 +132,22 @@ __global__ void __launch_bounds__(kStreamThreads) stream_kernel(const __grid_con
     const int c0 = (int)((int64_t)a.chunks * rank / a.splits);
     const int n = (int)((int64_t)a.chunks * (rank + 1) / a.splits) - c0;
 
-    if (threadIdx.x == 0) {
+    if (warp == 0 && elect_one()) {
+        prefetch_map(&wmap);
+        prefetch_map(&xmap);
+        if constexpr (kGated) prefetch_map(&umap);
+        for (int i = 0; i < min(n, a.ring); ++i) {
+            tma_prefetch_2d(&wmap, (c0 + i) * kChunkK, row0);
+            if constexpr (kGated) tma_prefetch_2d(&umap, (c0 + i) * kChunkK, row0);
+        }
+    }
+    if (threadIdx.x == 32) {
         abort_flag = 0;
         for (int i = 0; i < a.ring; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], kGated ? 2 : 1);
         }
-        mbar_init(&done, 1);
+        mbar_init(&done, 2);
         fence_mbar_init();
     }
     griddep_wait();
@@ -156,73 +185,78 @@ __global__ void __launch_bounds__(kStreamThreads) stream_kernel(const __grid_con
                 if (!(a.stall && blockIdx.x == 0 && i == 0))
                     mbar_wait_landed(&full[i % a.ring], (uint32_t)(i / a.ring) & 1);
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp <= 2) {
+        // Two warps multiply, into accumulators of their own (added up below;
+        // for the gated form one has W_gate, the other W_up): the waits, the
+        // four products and the commit of a chunk take one warp 540 cycles,
+        // 34 bytes of W a cycle, where an SM's share of the memory can be more.
+        // A plain unit's warps take the chunks in turn, so its ring has an even
+        // number of stages: each stage then belongs to one warp, which sees
+        // every phase of its barrier.  (A warp that came back to a stage two
+        // laps later would take the phase before last for the last one.)
+        const int me = warp - 1;
         const uint32_t idesc = make_idesc_bf16(kTileM, (uint32_t)a.tile, 0u, 0u);
         const uint64_t desc = make_sdesc(smem_u32(ring), 16u, 1024u, kLayoutSw128);
-        const uint32_t xoff = ((kGated ? 2 : 1) * kWTile) >> 4;
-        int s = 0, part = 0, until = 0;         // the part that chunk i belongs to ends before chunk `until`
+        const uint32_t woff = kGated ? (uint32_t)me * (kWTile >> 4) : 0u, xoff = ((kGated ? 2 : 1) * kWTile) >> 4;
+        const int mine = kGated ? n : (n + 1 - me) / 2;         // chunks: all, or every other
+        int s = kGated ? 0 : me, part = 0, until = 0;           // the part that chunk i belongs to ends before chunk `until`
         uint32_t lap = 0;
-        for (int i = 0; i < n; ++i) {
+        for (int i = 0; i < mine; ++i) {
             if (!mbar_wait_warp(&full[s], lap, &abort_flag)) break;
             const bool fresh = i == until;
             if (fresh) {
                 if (i) ++part;
-                until = (int)((int64_t)n * (part + 1) / a.parts);
+                until = (int)((int64_t)mine * (part + 1) / a.parts);
             }
             if (elect_one()) {
-                const uint64_t w = desc + (uint64_t)(s * (int)(a.stage_bytes >> 4)), x = w + xoff;
-                const uint32_t d = tmem + (uint32_t)(part * a.tile);
+                const uint64_t at = desc + (uint64_t)(s * (int)(a.stage_bytes >> 4));
+                const uint64_t w = at + woff, x = at + xoff;
+                const uint32_t d = tmem + (uint32_t)((me * a.parts + part) * a.tile);
 #pragma unroll
-                for (int kk = 0; kk < kChunkK / 16; ++kk) {
-                    const uint32_t acc = fresh && kk == 0 ? 0u : 1u;
-                    tc_mma_bf16(d, w + kk * 2, x + kk * 2, idesc, acc);
-                    if constexpr (kGated)
-                        tc_mma_bf16(d + (uint32_t)a.tile, w + (kWTile >> 4) + kk * 2, x + kk * 2, idesc, acc);
-                }
+                for (int kk = 0; kk < kChunkK / 16; ++kk)
+                    tc_mma_bf16(d, w + kk * 2, x + kk * 2, idesc, fresh && kk == 0 ? 0u : 1u);
                 tc_commit(&empty[s]);
-                if (i == n - 1) tc_commit(&done);
             }
             __syncwarp();
-            if (++s == a.ring) { s = 0; lap ^= 1; }
+            s += kGated ? 1 : 2;
+            if (s >= a.ring) { s -= a.ring; lap ^= 1; }
         }
-        if (__any_sync(0xffffffffu, *(volatile int*)&abort_flag)) {
-            if (elect_one()) tc_commit(&done);
-            mbar_wait_landed(&done, 0);
-        }
+        if (elect_one()) tc_commit(&done);          // at once where nothing was issued
+        if (__any_sync(0xffffffffu, *(volatile int*)&abort_flag)) mbar_wait_landed(&done, 0);
         __syncwarp();
     }
 
     // The partial sums, [token][128 rows] fp32, over the ring: every load has
-    // been consumed once the last product is done.
+    // been consumed once the last product is done.  A warp takes its quarter of
+    // the accumulator's lanes and every other 16 tokens.
     float* part = reinterpret_cast<float*>(ring);
-    if (warp >= 2) {
-        const bool ok = mbar_wait_hot(&done, 0, &abort_flag) && !*(volatile int*)&abort_flag;
-        if (__all_sync(0xffffffffu, ok)) {
-            tc_fence_after();
-            const int q = warp & 3;
-            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+    const bool ok = mbar_wait_hot(&done, 0, &abort_flag) && !*(volatile int*)&abort_flag;
+    if (__all_sync(0xffffffffu, ok)) {
+        tc_fence_after();
+        const int q = warp & 3;
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
 #pragma unroll
-            for (int m = 0; m < (kGated ? 2 : 1); ++m) {
-                float* p = part + m * a.tile * kTileM + q * 32 + lane;
-                for (int t = 0; t < ntok; t += 16) {
-                    uint32_t v[16];
-                    float sum[16];
-                    tc_ld_x16(lanes + (uint32_t)(m * a.tile + t), v);
+        for (int m = 0; m < (kGated ? 2 : 1); ++m) {
+            const int sums = kGated ? 1 : n > 1 ? 2 * a.parts : 1;
+            float* p = part + m * a.tile * kTileM + q * 32 + lane;
+            for (int t = (warp >> 2) * 16; t < ntok; t += 32) {
+                uint32_t v[16];
+                float sum[16];
+                tc_ld_x16(lanes + (uint32_t)(m * a.tile + t), v);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum[i] = __uint_as_float(v[i]);
+                for (int j = 1; j < sums; ++j) {
+                    tc_ld_x16(lanes + (uint32_t)(j * a.tile + t), v);
                     tc_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) sum[i] = __uint_as_float(v[i]);
-                    for (int j = 1; j < a.parts; ++j) {
-                        tc_ld_x16(lanes + (uint32_t)(j * a.tile + t), v);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) sum[i] += __uint_as_float(v[i]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) p[(t + i) * kTileM] = sum[i];
+                    for (int i = 0; i < 16; ++i) sum[i] += __uint_as_float(v[i]);
                 }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) p[(t + i) * kTileM] = sum[i];
             }
-            tc_fence_before();
         }
+        tc_fence_before();
     }
     __syncthreads();
     if (warp == 1) {
@@ -231,37 +265,17 @@ __global__ void __launch_bounds__(kStreamThreads) stream_kernel(const __grid_con
     }
     if (a.splits > 1) cluster_sync();
 
-    // Groups of 8 rows of W (outputs) of one token, spread over the cluster.
+    // Groups of 8 rows of W (outputs) of one token, spread over the cluster;
+    // the partials of all its CTAs are loaded before they are added.
     const uint32_t base = smem_u32(part);
     const bool fine = !*(volatile int*)&abort_flag;
     for (int g = rank * kStreamThreads + (int)threadIdx.x; g < ntok * (kTileM / 8); g += a.splits * kStreamThreads) {
         const int t = g / (kTileM / 8), o = (g & (kTileM / 8 - 1)) * 8;
         if (row0 + o >= a.N) continue;
-        float v[8] = {}, u[8] = {};
+        float v[8], u[8];
         const uint32_t at = base + (uint32_t)(t * kTileM + o) * 4u;
-        if (a.splits > 1) {
-#pragma unroll
-            for (int r = 0; r < kMaxSplits; ++r) {
-                if (r >= a.splits) break;
-                const uint32_t p = cluster_map(at, (uint32_t)r);
-                const float4 x0 = ld_cluster_v4(p), x1 = ld_cluster_v4(p + 16);
-                v[0] += x0.x; v[1] += x0.y; v[2] += x0.z; v[3] += x0.w;
-                v[4] += x1.x; v[5] += x1.y; v[6] += x1.z; v[7] += x1.w;
-                if constexpr (kGated) {
-                    const uint32_t pu = p + (uint32_t)(a.tile * kTileM) * 4u;
-                    const float4 y0 = ld_cluster_v4(pu), y1 = ld_cluster_v4(pu + 16);
-                    u[0] += y0.x; u[1] += y0.y; u[2] += y0.z; u[3] += y0.w;
-                    u[4] += y1.x; u[5] += y1.y; u[6] += y1.z; u[7] += y1.w;
-                }
-            }
-        } else {
-            const float* p = part + t * kTileM + o;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[i] = p[i];
-                if constexpr (kGated) u[i] = p[a.tile * kTileM + i];
-            }
-        }
+        sum_partials(v, at, a.splits);
+        if constexpr (kGated) sum_partials(u, at + (uint32_t)(a.tile * kTileM) * 4u, a.splits);
         if (fine) finish8<kGated>(a, v, u, t0 + t, row0 + o);
     }
     if (threadIdx.x == 0 && !fine && a.status) atomicOr(a.status, ADAFUSE_STATUS_TIMEOUT);
@@ -312,7 +326,8 @@ int launch_stream(ProjectCall& c)
     a.tile = (int)(((a.T + a.n_tt - 1) / a.n_tt + 15) / 16 * 16);
     const auto ring_of = [&](bool half) {
         a.stage_bytes = (kGated ? 2 : 1) * kWTile + (uint32_t)a.tile * kChunkK * 2;
-        return (int)std::min<uint32_t>(kMaxRing, ((half ? kSmemHalf : kSmemFull) - 1024) / a.stage_bytes);
+        const int most = (int)std::min<uint32_t>(kMaxRing, ((half ? kSmemHalf : kSmemFull) - 1024) / a.stage_bytes);
+        return kGated ? most : most & ~1;           // plain: even, see the multiplying warps
     };
     // Two CTAs per SM keep more units in flight; taller tiles need the whole
     // shared memory for four stages and their partial sums.
@@ -330,14 +345,15 @@ int launch_stream(ProjectCall& c)
         if (!a.splits || cost < best) best = cost, a.splits = S;
     }
     if (!a.splits) return ADAFUSE_ERR_CUDA;
+    // accumulators of a plain unit: `parts` for each of the two multiplying warps
     a.parts = 1;
     if (a.y_f32) {
         const int per = (a.chunks + a.splits - 1) / a.splits;
-        a.parts = std::min((half ? 256 : 512) / a.tile, (per * kChunkK + kPartCols - 1) / kPartCols);
-        a.parts = std::max(1, std::min(a.parts, a.chunks / a.splits));
+        a.parts = std::min((half ? 256 : 512) / (2 * a.tile), (per * kChunkK / 2 + kPartCols - 1) / kPartCols);
+        a.parts = std::max(1, std::min(a.parts, a.chunks / a.splits / 2));
     }
     a.tmem_cols = 32;
-    while ((int)a.tmem_cols < a.tile * a.parts * (kGated ? 2 : 1)) a.tmem_cols *= 2;
+    while ((int)a.tmem_cols < a.tile * a.parts * 2) a.tmem_cols *= 2;
     if (blocks * a.splits > 0x7fffffff) return ADAFUSE_ERR_UNSUPPORTED;
 
     CUtensorMap xm, wm, um;

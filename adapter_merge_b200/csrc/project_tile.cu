@@ -48,30 +48,6 @@ struct TileArgs : ProjectArgs {
     int64_t tiles;
 };
 
-template <int N>
-__device__ __forceinline__ void activate_all(float (&v)[N], uint32_t act)
-{
-    switch (act) {
-        case ADAFUSE_ACT_NONE: return;
-        case ADAFUSE_ACT_RELU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = activate(v[i], ADAFUSE_ACT_RELU);
-            return;
-        case ADAFUSE_ACT_SILU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = activate(v[i], ADAFUSE_ACT_SILU);
-            return;
-        case ADAFUSE_ACT_GELU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = activate(v[i], ADAFUSE_ACT_GELU);
-            return;
-        default:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = activate(v[i], ADAFUSE_ACT_GELU_TANH);
-            return;
-    }
-}
-
 // Adds p[0 .. N) (bf16, 16-byte aligned) to v; groups of 8 from `limit` on are not read.
 template <int N>
 __device__ __forceinline__ void add_bf16(float (&v)[N], const uint16_t* p, int limit)

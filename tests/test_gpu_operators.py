@@ -112,6 +112,16 @@ def test_project_widths(am, K, N):
     check_project(am, 130, K, N, f32=True, seed=3)
 
 
+@pytest.mark.parametrize("T", [1, 17, 33, 48, 64, 80, 96, 112, 128, 144, 160, 176, 192, 208, 224, 240, 256, 272, 500])
+def test_projections_over_many_laps_of_a_ring(am, T):
+    """Rings of every depth, walked many times by one CTA, alone and in clusters."""
+    check_project(am, T, 13824, 128, seed=T)
+    check_project(am, T, 8192, 1024, f32=True, seed=T)
+    check_project(am, T, 2048, 13824, seed=T)
+    check_gated(am, T, 13824, 128, seed=T)
+    check_gated(am, T, 2048, 13824, seed=T)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("T", [3, 270])
 def test_project_activations(am, act, T):
