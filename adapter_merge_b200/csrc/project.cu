@@ -60,55 +60,86 @@ struct StreamArgs : ProjectArgs {
     uint32_t tmem_cols, stage_bytes;
 };
 
-// bias, activation, product and residual of 8 consecutive outputs, and their store
+// bias, activation, product and residual of 4 consecutive outputs, and their store
 template <bool kGated>
-__device__ __forceinline__ void finish8(const StreamArgs& a, float (&v)[8], float (&u)[8], int64_t t, int o)
+__device__ __forceinline__ void finish4(const StreamArgs& a, float (&v)[4], float (&u)[4], int64_t t, int o)
 {
-    const auto add = [](float (&d)[8], const uint16_t* p) {
-        const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const auto add = [](float (&d)[4], const uint16_t* p) {
+        const uint2 w = *reinterpret_cast<const uint2*>(p);
         d[0] += bf16lo(w.x); d[1] += bf16hi(w.x); d[2] += bf16lo(w.y); d[3] += bf16hi(w.y);
-        d[4] += bf16lo(w.z); d[5] += bf16hi(w.z); d[6] += bf16lo(w.w); d[7] += bf16hi(w.w);
     };
     if (a.bias) add(v, a.bias + o);
     activate_all(v, a.act);
     if constexpr (kGated) {
         if (a.bias_up) add(u, a.bias_up + o);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= u[i];
+        for (int i = 0; i < 4; ++i) v[i] *= u[i];
     } else {
         if (a.residual) add(v, a.residual + t * a.ldr + o);
     }
-    if (!kGated && a.y_f32) {
-        float* p = static_cast<float*>(a.y) + t * a.ldy + o;
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        uint16_t* p = static_cast<uint16_t*>(a.y) + t * a.ldy + o;
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    if (!kGated && a.y_f32)
+        *reinterpret_cast<float4*>(static_cast<float*>(a.y) + t * a.ldy + o) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + t * a.ldy + o) =
+            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+
+// v[j] = the sum over the cluster's CTAs, in rank order, of the 4 floats at
+// `at` + j * step in their shared memory, j < count.  Four CTAs' values of all
+// j are loaded before they are added: a remote load takes about 700 cycles.
+template <int U>
+__device__ __forceinline__ void sum_partials(float (&v)[U][4], uint32_t at, uint32_t step, int count, int splits)
+{
+    constexpr int kAhead = 4;
+    if (splits == 1) {
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (j < count) {
+                const uint4 x = ld_shared_v4(at + (uint32_t)j * step);
+                v[j][0] = __uint_as_float(x.x); v[j][1] = __uint_as_float(x.y);
+                v[j][2] = __uint_as_float(x.z); v[j][3] = __uint_as_float(x.w);
+            }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = 0.f;
+    for (int r0 = 0; r0 < splits; r0 += kAhead) {
+        float4 x[U][kAhead];
+#pragma unroll
+        for (int r = 0; r < kAhead; ++r) {
+            const uint32_t p = cluster_map(at, (uint32_t)min(r0 + r, splits - 1));
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                x[j][r] = j < count && r0 + r < splits ? ld_cluster_v4(p + (uint32_t)j * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int r = 0; r < kAhead; ++r)
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                v[j][0] += x[j][r].x; v[j][1] += x[j][r].y; v[j][2] += x[j][r].z; v[j][3] += x[j][r].w;
+            }
     }
 }
 
-// The 8 floats at this address in each CTA of the cluster, added in rank order.
-__device__ __forceinline__ void sum_partials(float (&v)[8], uint32_t at, int splits)
+// Tokens first, first + gap, ... of a unit's `ntok`: sums, epilogue and store, U tokens at a time.
+template <bool kGated, int U>
+__device__ __forceinline__ void finish_tokens(const StreamArgs& a, uint32_t part, int first, int gap, int ntok, int64_t t0,
+                                              int row0, bool fine)
 {
-    float4 x[kMaxSplits][2];
+    const int lane = threadIdx.x & 31, o = row0 + lane * 4;
+    const uint32_t step = (uint32_t)(gap * kTileM) * 4u;
+    for (int t = first; t < ntok; t += U * gap) {
+        float v[U][4], u[U][4];
+        const uint32_t at = part + (uint32_t)(t * kTileM + lane * 4) * 4u;
+        const int count = (ntok - t + gap - 1) / gap;
+        sum_partials<U>(v, at, step, count, a.splits);
+        if constexpr (kGated) sum_partials<U>(u, at + (uint32_t)(a.tile * kTileM) * 4u, step, count, a.splits);
+        if (!fine || o >= a.N) continue;
 #pragma unroll
-    for (int r = 0; r < kMaxSplits; ++r) {
-        if (r < splits) {
-            const uint32_t p = splits > 1 ? cluster_map(at, (uint32_t)r) : at;
-            x[r][0] = ld_cluster_v4(p);
-            x[r][1] = ld_cluster_v4(p + 16);
-        } else {
-            x[r][0] = x[r][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-#pragma unroll
-    for (int r = 0; r < kMaxSplits; ++r) {
-        v[0] += x[r][0].x; v[1] += x[r][0].y; v[2] += x[r][0].z; v[3] += x[r][0].w;
-        v[4] += x[r][1].x; v[5] += x[r][1].y; v[6] += x[r][1].z; v[7] += x[r][1].w;
+        for (int j = 0; j < U; ++j)
+            if (j < count) finish4<kGated>(a, v[j], u[j], t0 + t + (int64_t)j * gap, o);
     }
 }
 
@@ -265,19 +296,15 @@ __global__ void __launch_bounds__(kStreamThreads, 2) stream_kernel(const __grid_
     }
     if (a.splits > 1) cluster_sync();
 
-    // Groups of 8 rows of W (outputs) of one token, spread over the cluster;
-    // the partials of all its CTAs are loaded before they are added.
-    const uint32_t base = smem_u32(part);
+    // A warp takes a token's 128 outputs, four per lane; the cluster's warps
+    // share the tokens, each with four tokens under way where there are more
+    // tokens than warps.
+    constexpr int kWarps = kStreamThreads / 32;
     const bool fine = !*(volatile int*)&abort_flag;
-    for (int g = rank * kStreamThreads + (int)threadIdx.x; g < ntok * (kTileM / 8); g += a.splits * kStreamThreads) {
-        const int t = g / (kTileM / 8), o = (g & (kTileM / 8 - 1)) * 8;
-        if (row0 + o >= a.N) continue;
-        float v[8], u[8];
-        const uint32_t at = base + (uint32_t)(t * kTileM + o) * 4u;
-        sum_partials(v, at, a.splits);
-        if constexpr (kGated) sum_partials(u, at + (uint32_t)(a.tile * kTileM) * 4u, a.splits);
-        if (fine) finish8<kGated>(a, v, u, t0 + t, row0 + o);
-    }
+    if (ntok <= a.splits * kWarps)
+        finish_tokens<kGated, 1>(a, smem_u32(part), rank * kWarps + warp, a.splits * kWarps, ntok, t0, row0, fine);
+    else
+        finish_tokens<kGated, 4>(a, smem_u32(part), rank * kWarps + warp, a.splits * kWarps, ntok, t0, row0, fine);
     if (threadIdx.x == 0 && !fine && a.status) atomicOr(a.status, ADAFUSE_STATUS_TIMEOUT);
     if (a.splits > 1) cluster_sync();       // the others may still read this CTA's partials
 }
@@ -288,12 +315,14 @@ __global__ void __launch_bounds__(kStreamThreads, 2) stream_kernel(const __grid_
 // an SM, or one.
 constexpr uint32_t kSmemHalf = 111 * 1024, kSmemFull = 225 * 1024;
 
-// Clusters of `splits` CTAs that the device runs at a time, asked once.
+// Clusters of `splits` CTAs, one CTA per SM, that the device runs at a time,
+// asked once.  (For CTAs of half an SM the runtime gives the same number, but
+// two do share an SM: 157 of them, 20000 outputs, end in one round.)
 template <bool kGated>
-int clusters_at_once(int dev, int splits, bool half)
+int clusters_at_once(int dev, int splits)
 {
-    static std::atomic<int> known[16][2][kMaxSplits + 1];
-    std::atomic<int>* slot = dev < 16 ? &known[dev][half][splits] : nullptr;
+    static std::atomic<int> known[16][kMaxSplits + 1];
+    std::atomic<int>* slot = dev < 16 ? &known[dev][splits] : nullptr;
     int v = slot ? slot->load(std::memory_order_relaxed) : 0;
     if (v > 0) return v;
     auto kernel = stream_kernel<kGated>;
@@ -306,7 +335,7 @@ int clusters_at_once(int dev, int splits, bool half)
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)splits);
     cfg.blockDim = dim3(kStreamThreads);
-    cfg.dynamicSmemBytes = half ? kSmemHalf : kSmemFull;
+    cfg.dynamicSmemBytes = kSmemFull;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaOccupancyMaxActiveClusters(&v, kernel, &cfg) != cudaSuccess || v < 1) return 0;
@@ -329,21 +358,35 @@ int launch_stream(ProjectCall& c)
         const int most = (int)std::min<uint32_t>(kMaxRing, ((half ? kSmemHalf : kSmemFull) - 1024) / a.stage_bytes);
         return kGated ? most : most & ~1;           // plain: even, see the multiplying warps
     };
-    // Two CTAs per SM keep more units in flight; taller tiles need the whole
-    // shared memory for four stages and their partial sums.
-    const bool half = a.tile <= 64;
-    a.ring = ring_of(half);
-    // The split of d_in that ends first: as many rounds of clusters as the
-    // device needs, each as long as its chunks and a fixed part.
+    // One CTA per SM with a deep ring, or two (tiles of up to 64 tokens, whose
+    // partial sums fit half of shared memory), and the split of d_in that ends
+    // first, in cycles.  Measured: a chunk takes a CTA 365 cycles (gated 500),
+    // more for tall tiles; memory gives W's bytes at 3400 a cycle where two
+    // thirds of the SMs' places are taken, less below; the sum over the splits,
+    // and each further round of clusters, cost their part.  (4096 -> 11008, one
+    // token: 17.6 us as two CTAs per SM in three splits, 19.6 as one without;
+    // 64 tokens: 21.0 and 23.7; 5120 -> 13824, 32 tokens: 29.2 and 27.7.)
+    const double places = device_sms();
     const int64_t blocks = (int64_t)((a.N + kTileM - 1) / kTileM) * a.n_tt;
+    const double tall = a.tile * (kGated ? 2. : 1.);
+    const double chunk = kGated ? std::max(500., 4 * tall) : std::max(365., 2.9 * tall);
+    const double memory = (kGated ? 4. : 2.) * a.N * c.K * a.n_tt / 3400;
     double best = 0;
+    bool half = false;
     a.splits = 0;
-    for (int S = 1; S <= kMaxSplits && S <= a.chunks; ++S) {
-        const int at_once = clusters_at_once<kGated>(dev, S, half);
-        if (!at_once) continue;
-        const double cost = (double)((blocks + at_once - 1) / at_once) * ((a.chunks + S - 1) / S + 6);
-        if (!a.splits || cost < best) best = cost, a.splits = S;
-    }
+    for (int two = 0; two <= (a.tile <= 64 ? 1 : 0); ++two)
+        for (int S = 1; S <= kMaxSplits && S <= a.chunks; ++S) {
+            const int at_once = clusters_at_once<kGated>(dev, S) * (1 + two);
+            if (!at_once) continue;
+            const int64_t rounds = (blocks + at_once - 1) / at_once;
+            const double taken = (double)blocks * S / (rounds * places * (1 + two));
+            const double work = (double)rounds * ((a.chunks + S - 1) / S) * chunk * (two ? 1.6 : 1.);
+            const double stream = memory / std::min(1., taken / 0.67);
+            const double cost = std::max(work, stream) + std::min(work, stream) / 4 + (300 + 3 * tall) * S +
+                                (rounds - 1) * (5000 + 40 * tall) + two * 2500;
+            if (!a.splits || cost < best) best = cost, a.splits = S, half = two;
+        }
+    a.ring = ring_of(half);
     if (!a.splits) return ADAFUSE_ERR_CUDA;
     // accumulators of a plain unit: `parts` for each of the two multiplying warps
     a.parts = 1;
