@@ -84,62 +84,24 @@ __device__ __forceinline__ void finish4(const StreamArgs& a, float (&v)[4], floa
             make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
-// v[j] = the sum over the cluster's CTAs, in rank order, of the 4 floats at
-// `at` + j * step in their shared memory, j < count.  Four CTAs' values of all
-// j are loaded before they are added: a remote load takes about 700 cycles.
-template <int U>
-__device__ __forceinline__ void sum_partials(float (&v)[U][4], uint32_t at, uint32_t step, int count, int splits)
+// v += 4 floats in shared memory
+__device__ __forceinline__ void add4(float (&v)[4], uint32_t at)
 {
-    constexpr int kAhead = 4;
-    if (splits == 1) {
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-            if (j < count) {
-                const uint4 x = ld_shared_v4(at + (uint32_t)j * step);
-                v[j][0] = __uint_as_float(x.x); v[j][1] = __uint_as_float(x.y);
-                v[j][2] = __uint_as_float(x.z); v[j][3] = __uint_as_float(x.w);
-            }
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < U; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] = 0.f;
-    for (int r0 = 0; r0 < splits; r0 += kAhead) {
-        float4 x[U][kAhead];
-#pragma unroll
-        for (int r = 0; r < kAhead; ++r) {
-            const uint32_t p = cluster_map(at, (uint32_t)min(r0 + r, splits - 1));
-#pragma unroll
-            for (int j = 0; j < U; ++j)
-                x[j][r] = j < count && r0 + r < splits ? ld_cluster_v4(p + (uint32_t)j * step) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int r = 0; r < kAhead; ++r)
-#pragma unroll
-            for (int j = 0; j < U; ++j) {
-                v[j][0] += x[j][r].x; v[j][1] += x[j][r].y; v[j][2] += x[j][r].z; v[j][3] += x[j][r].w;
-            }
-    }
+    const uint4 x = ld_shared_v4(at);
+    v[0] += __uint_as_float(x.x); v[1] += __uint_as_float(x.y);
+    v[2] += __uint_as_float(x.z); v[3] += __uint_as_float(x.w);
 }
 
-// Tokens first, first + gap, ... of a unit's `ntok`: sums, epilogue and store, U tokens at a time.
-template <bool kGated, int U>
-__device__ __forceinline__ void finish_tokens(const StreamArgs& a, uint32_t part, int first, int gap, int ntok, int64_t t0,
-                                              int row0, bool fine)
+// v = the sum, in rank order, of the 4 floats at `mine` (this CTA's) and those
+// of the cluster's other CTAs, `step` bytes apart from `theirs` on.
+__device__ __forceinline__ void sum_ranks(float (&v)[4], uint32_t mine, uint32_t theirs, uint32_t step, int rank, int splits)
 {
-    const int lane = threadIdx.x & 31, o = row0 + lane * 4;
-    const uint32_t step = (uint32_t)(gap * kTileM) * 4u;
-    for (int t = first; t < ntok; t += U * gap) {
-        float v[U][4], u[U][4];
-        const uint32_t at = part + (uint32_t)(t * kTileM + lane * 4) * 4u;
-        const int count = (ntok - t + gap - 1) / gap;
-        sum_partials<U>(v, at, step, count, a.splits);
-        if constexpr (kGated) sum_partials<U>(u, at + (uint32_t)(a.tile * kTileM) * 4u, step, count, a.splits);
-        if (!fine || o >= a.N) continue;
 #pragma unroll
-        for (int j = 0; j < U; ++j)
-            if (j < count) finish4<kGated>(a, v[j], u[j], t0 + t + (int64_t)j * gap, o);
+    for (int i = 0; i < 4; ++i) v[i] = 0.f;
+#pragma unroll
+    for (int r = 0; r < kMaxSplits; ++r) {
+        if (r >= splits) break;
+        add4(v, r == rank ? mine : theirs + (uint32_t)(r < rank ? r : r - 1) * step);
     }
 }
 
@@ -150,7 +112,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) stream_kernel(const __grid_
                                                                 const StreamArgs a)
 {
     extern __shared__ uint8_t dyn[];
-    __shared__ uint64_t full[kMaxRing], empty[kMaxRing], done;
+    __shared__ uint64_t full[kMaxRing], empty[kMaxRing], done, joined;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
@@ -179,6 +141,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) stream_kernel(const __grid_
             mbar_init(&empty[i], kGated ? 2 : 1);
         }
         mbar_init(&done, 2);
+        mbar_init(&joined, 1);
         fence_mbar_init();
     }
     griddep_wait();
@@ -289,24 +252,57 @@ __global__ void __launch_bounds__(kStreamThreads, 2) stream_kernel(const __grid_
         }
         tc_fence_before();
     }
+    fence_proxy_async_smem();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, a.tmem_cols);
     }
-    if (a.splits > 1) cluster_sync();
 
-    // A warp takes a token's 128 outputs, four per lane; the cluster's warps
-    // share the tokens, each with four tokens under way where there are more
-    // tokens than warps.
-    constexpr int kWarps = kStreamThreads / 32;
-    const bool fine = !*(volatile int*)&abort_flag;
-    if (ntok <= a.splits * kWarps)
-        finish_tokens<kGated, 1>(a, smem_u32(part), rank * kWarps + warp, a.splits * kWarps, ntok, t0, row0, fine);
-    else
-        finish_tokens<kGated, 4>(a, smem_u32(part), rank * kWarps + warp, a.splits * kWarps, ntok, t0, row0, fine);
+    // Each CTA of the cluster finishes its share of the tokens: the others copy
+    // their partial sums of them behind its own, one bulk copy each (remote
+    // loads by its threads brought 12 bytes a cycle).
+    constexpr int kParts = kGated ? 2 : 1;
+    const int own = (a.tile + a.splits - 1) / a.splits;
+    const uint32_t sums = smem_u32(part), theirs = sums + (uint32_t)(kParts * a.tile * kTileM) * 4u;
+    const uint32_t step = (uint32_t)(kParts * own * kTileM) * 4u;        // of one other CTA's sums
+    const auto tokens_of = [&](int r) { return max(0, min(own, ntok - r * own)); };
+    const int here = tokens_of(rank);
+    bool ours = true;
+    if (a.splits > 1) {
+        if (threadIdx.x == 0 && here)
+            mbar_arrive_expect_tx(&joined, (uint32_t)((a.splits - 1) * kParts * here * kTileM) * 4u);
+        cluster_sync();             // every ring is free, every partial sum written
+        if (warp == 0 && elect_one())
+            for (int r = 0; r < a.splits; ++r) {
+                const int count = tokens_of(r);
+                if (r == rank || !count) continue;
+                const uint32_t to = cluster_map(theirs + (uint32_t)(rank < r ? rank : rank - 1) * step, (uint32_t)r);
+                for (int m = 0; m < kParts; ++m)
+                    bulk_copy_cluster(to + (uint32_t)(m * own * kTileM) * 4u,
+                                      sums + (uint32_t)((m * a.tile + r * own) * kTileM) * 4u,
+                                      (uint32_t)(count * kTileM) * 4u, cluster_map(smem_u32(&joined), (uint32_t)r));
+            }
+        __syncwarp();
+        ours = !here || mbar_wait_hot(&joined, 0, &abort_flag);
+        cluster_arrive();           // what came here has left the others
+    }
+    // A warp takes a token's 128 outputs, four per lane.
+    const bool fine = ours && !*(volatile int*)&abort_flag;
+    const int o = row0 + lane * 4;
+    if (fine && o < a.N)
+        for (int i = warp; i < here; i += kStreamThreads / 32) {
+            float v[4], u[4];
+            const uint32_t at = (uint32_t)(i * kTileM + lane * 4) * 4u;
+            const uint32_t mine = sums + (uint32_t)(rank * own * kTileM) * 4u + at;
+            sum_ranks(v, mine, theirs + at, step, rank, a.splits);
+            if constexpr (kGated)
+                sum_ranks(u, mine + (uint32_t)(a.tile * kTileM) * 4u, theirs + (uint32_t)(own * kTileM) * 4u + at, step,
+                          rank, a.splits);
+            finish4<kGated>(a, v, u, t0 + rank * own + i, o);
+        }
     if (threadIdx.x == 0 && !fine && a.status) atomicOr(a.status, ADAFUSE_STATUS_TIMEOUT);
-    if (a.splits > 1) cluster_sync();       // the others may still read this CTA's partials
+    if (a.splits > 1) cluster_wait();       // the others' copies of this CTA's sums are done
 }
 
 // ------------------------------------------------------------------ host side
@@ -343,56 +339,81 @@ int clusters_at_once(int dev, int splits)
     return v;
 }
 
+// How a call runs on the stream kernel.
+struct StreamForm {
+    int tile = 0, n_tt = 0, splits = 0, ring = 0;
+    bool half = false;
+    double cost = 0;            // estimated cycles
+};
+
+// The cheapest form: tiles of up to 128 tokens (gated 64) or twice that; one
+// CTA per SM with a deep ring, or two (where a ring and the partial sums fit
+// half of shared memory); and the split of d_in.  Measured: a chunk takes a CTA
+// 365 cycles (gated 500), more for tall tiles; memory gives W's bytes at 3400 a
+// cycle where two thirds of the SMs' places are taken, less below; the sum over
+// the splits, and each further round of clusters, cost their part.  (4096 ->
+// 11008, one token: 17.6 us as two CTAs per SM in three splits, 19.6 as one
+// without; 64 tokens: 20.8 and 22.7; 5120 -> 13824, 32 tokens: 28.7 and 27.4.
+// 256 tokens, 4096 -> 4096: 16.2 us as two tiles, 19.2 as one; 4096 -> 11008:
+// 48 and 43.)
 template <bool kGated>
-int launch_stream(ProjectCall& c)
+StreamForm stream_form(const ProjectCall& c, int dev)
+{
+    StreamForm best;
+    const ProjectArgs& a = c.a;
+    const double places = device_sms();
+    constexpr int kMats = kGated ? 2 : 1;
+    int last = 0;
+    for (int most = 128 / kMats; most <= 256 / kMats; most *= 2) {
+        StreamForm f;
+        f.n_tt = (int)((a.T + most - 1) / most);
+        if (f.n_tt == last) break;
+        last = f.n_tt;
+        f.tile = (int)(((a.T + f.n_tt - 1) / f.n_tt + 15) / 16 * 16);       // of equal height
+        const uint32_t stage = kMats * kWTile + (uint32_t)f.tile * kChunkK * 2;
+        const int64_t blocks = (int64_t)((a.N + kTileM - 1) / kTileM) * f.n_tt;
+        const double tall = f.tile * kMats;
+        const double chunk = kGated ? std::max(500., 4 * tall) : std::max(365., 2.9 * tall);
+        const double memory = 2. * kMats * a.N * c.K / 3400;
+        for (int two = 0; two < 2; ++two)
+            for (int S = 1; S <= kMaxSplits && S <= a.chunks; ++S) {
+                // its own and the others' partial sums lie over the ring in the end
+                const uint32_t room = (two ? kSmemHalf : kSmemFull) - 1024;
+                const uint32_t sums = (uint32_t)(f.tile + (f.tile + S - 1) / S * (S - 1)) * kTileM * 4 * kMats;
+                f.ring = (int)std::min<uint32_t>(kMaxRing, room / stage);
+                if (!kGated) f.ring &= ~1;              // even, see the multiplying warps
+                if (sums > room || f.ring < (kGated ? 3 : 4)) continue;
+                const int at_once = clusters_at_once<kGated>(dev, S) * (1 + two);
+                if (!at_once) continue;
+                const int64_t rounds = (blocks + at_once - 1) / at_once;
+                const double taken = (double)blocks * S / (rounds * places * (1 + two));
+                const double work = (double)rounds * ((a.chunks + S - 1) / S) * chunk * (two ? 1.6 : 1.);
+                const double stream = memory / std::min(1., taken / 0.67);
+                f.cost = std::max(work, stream) + std::min(work, stream) / 8 + (300 + 3 * tall) * S +
+                         (double)rounds * (6500 + 45 * tall) + two * 2500;
+                f.splits = S;
+                f.half = two;
+                if (!best.splits || f.cost < best.cost) best = f;
+            }
+    }
+    return best;
+}
+
+template <bool kGated>
+int launch_stream(ProjectCall& c, const StreamForm& f)
 {
     StreamArgs a{c.a};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return ADAFUSE_ERR_DEVICE;
-    // the fewest token tiles, of equal height
-    const int most = kGated ? 128 : 256;
-    a.n_tt = (int)((a.T + most - 1) / most);
-    a.tile = (int)(((a.T + a.n_tt - 1) / a.n_tt + 15) / 16 * 16);
-    const auto ring_of = [&](bool half) {
-        a.stage_bytes = (kGated ? 2 : 1) * kWTile + (uint32_t)a.tile * kChunkK * 2;
-        const int most = (int)std::min<uint32_t>(kMaxRing, ((half ? kSmemHalf : kSmemFull) - 1024) / a.stage_bytes);
-        return kGated ? most : most & ~1;           // plain: even, see the multiplying warps
-    };
-    // One CTA per SM with a deep ring, or two (tiles of up to 64 tokens, whose
-    // partial sums fit half of shared memory), and the split of d_in that ends
-    // first, in cycles.  Measured: a chunk takes a CTA 365 cycles (gated 500),
-    // more for tall tiles; memory gives W's bytes at 3400 a cycle where two
-    // thirds of the SMs' places are taken, less below; the sum over the splits,
-    // and each further round of clusters, cost their part.  (4096 -> 11008, one
-    // token: 17.6 us as two CTAs per SM in three splits, 19.6 as one without;
-    // 64 tokens: 21.0 and 23.7; 5120 -> 13824, 32 tokens: 29.2 and 27.7.)
-    const double places = device_sms();
+    a.tile = f.tile;
+    a.n_tt = f.n_tt;
+    a.splits = f.splits;
+    a.ring = f.ring;
+    a.stage_bytes = (kGated ? 2 : 1) * kWTile + (uint32_t)a.tile * kChunkK * 2;
     const int64_t blocks = (int64_t)((a.N + kTileM - 1) / kTileM) * a.n_tt;
-    const double tall = a.tile * (kGated ? 2. : 1.);
-    const double chunk = kGated ? std::max(500., 4 * tall) : std::max(365., 2.9 * tall);
-    const double memory = (kGated ? 4. : 2.) * a.N * c.K * a.n_tt / 3400;
-    double best = 0;
-    bool half = false;
-    a.splits = 0;
-    for (int two = 0; two <= (a.tile <= 64 ? 1 : 0); ++two)
-        for (int S = 1; S <= kMaxSplits && S <= a.chunks; ++S) {
-            const int at_once = clusters_at_once<kGated>(dev, S) * (1 + two);
-            if (!at_once) continue;
-            const int64_t rounds = (blocks + at_once - 1) / at_once;
-            const double taken = (double)blocks * S / (rounds * places * (1 + two));
-            const double work = (double)rounds * ((a.chunks + S - 1) / S) * chunk * (two ? 1.6 : 1.);
-            const double stream = memory / std::min(1., taken / 0.67);
-            const double cost = std::max(work, stream) + std::min(work, stream) / 4 + (300 + 3 * tall) * S +
-                                (rounds - 1) * (5000 + 40 * tall) + two * 2500;
-            if (!a.splits || cost < best) best = cost, a.splits = S, half = two;
-        }
-    a.ring = ring_of(half);
-    if (!a.splits) return ADAFUSE_ERR_CUDA;
     // accumulators of a plain unit: `parts` for each of the two multiplying warps
     a.parts = 1;
     if (a.y_f32) {
         const int per = (a.chunks + a.splits - 1) / a.splits;
-        a.parts = std::min((half ? 256 : 512) / (2 * a.tile), (per * kChunkK / 2 + kPartCols - 1) / kPartCols);
+        a.parts = std::min((f.half ? 256 : 512) / (2 * a.tile), (per * kChunkK / 2 + kPartCols - 1) / kPartCols);
         a.parts = std::max(1, std::min(a.parts, a.chunks / a.splits / 2));
     }
     a.tmem_cols = 32;
@@ -405,17 +426,23 @@ int launch_stream(ProjectCall& c)
     if (!kGated) um = wm;
     else if (!encode_rows(&um, c.W_up, a.N, c.K, c.ldw, kTileM)) return ADAFUSE_ERR_UNSUPPORTED;
     return launch_pdl_cluster(stream_kernel<kGated>, dim3((unsigned)(blocks * a.splits)), dim3(kStreamThreads),
-                              half ? kSmemHalf : kSmemFull, a.splits, c.s, xm, wm, um, a);
+                              f.half ? kSmemHalf : kSmemFull, a.splits, c.s, xm, wm, um, a);
 }
 
-// Up to this many tokens W streams past them; above, tiles of tokens and
-// outputs on CTA pairs.
-constexpr int64_t kStreamTokens = 256;
+// Up to this many tokens W may stream past them; beyond, and where the estimate
+// is lower (4096 -> 4096 from 257 tokens on, 4096 -> 11008 from 129), tiles of
+// tokens and outputs on CTA pairs.
+constexpr int64_t kStreamTokens = 1024;
 
 template <bool kGated>
 int launch_project(ProjectCall& c)
 {
-    return c.a.T <= kStreamTokens ? launch_stream<kGated>(c) : launch_project_tile(c);
+    if (c.a.T > kStreamTokens) return launch_project_tile(c);
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ADAFUSE_ERR_DEVICE;
+    const StreamForm f = stream_form<kGated>(c, dev);
+    if (!f.splits || f.cost > project_tile_cost(c)) return launch_project_tile(c);
+    return launch_stream<kGated>(c, f);
 }
 
 int check(ProjectCall& c, const void* bias, const void* bias_up, bool gated, uint32_t flags)

@@ -35,5 +35,6 @@ constexpr int kPartCols = 512;
 bool encode_rows(CUtensorMap* m, const void* p, int64_t rows, int32_t cols, int64_t ld, int box_rows);
 
 int launch_project_tile(ProjectCall& c);
+double project_tile_cost(const ProjectCall& c);     // estimated cycles
 
 }  // namespace af

@@ -35,10 +35,15 @@ constexpr uint32_t kRowPitch = 80;              // 64 bytes of a row and 16 of p
 constexpr uint32_t kTurnBytes = kEpiWarps * 32 * kRowPitch;
 constexpr uint32_t kXBytes = 128 * kChunkK * 2; // a CTA's tokens of a chunk
 
+// A stage holds one chunk of a wide tile, two of a narrow one: the waits and
+// the commit of a stage, with four products of 128 columns, took the issuing
+// warp 500 cycles, as long as four of 256 columns take the tensor core.
 template <int kCols>
 struct Ring {
+    static constexpr int kPer = kCols == 128 ? 2 : 1;              // chunks per stage
     static constexpr uint32_t kWBytes = kCols / 2 * kChunkK * 2;
-    static constexpr uint32_t kStage = kXBytes + kWBytes;
+    static constexpr uint32_t kChunk = kXBytes + kWBytes;
+    static constexpr uint32_t kStage = kPer * kChunk;
     static constexpr int kStages = (int)((kTileSmem - 1024 - kTurnBytes) / kStage);
 };
 
@@ -184,7 +189,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         // (and, below, the products: issued from a branch of one lane, with the
         // others parked, a 64-column chunk of a 256 x 256 tile took 705 cycles
         // instead of the 505 that its products take).
-        int64_t it = 0;             // chunks so far
+        int64_t it = 0;             // stages so far
         int s = 0;                  // the ring's next stage
         uint32_t lap = 1;           // parity that its `empty` completes with when free (the first lap: at once)
         bool stop = false;
@@ -194,7 +199,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             const int t = m * kPairTokens + rank * 128;
             const int row = kGated ? n * a.out_cols : n * a.out_cols + rank * (kCols / 2);
             const CUtensorMap* w = kGated && rank ? &umap : &wmap;
-            for (int c = 0; c < a.chunks; ++c, ++it) {
+            for (int c = 0; c < a.chunks; c += R::kPer, ++it) {
                 if (!mbar_wait_warp(&empty[s], lap, &abort_flag)) {
                     stop = true;
                     break;
@@ -203,8 +208,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                     uint8_t* p = ring + (size_t)s * R::kStage;
                     const uint32_t bar = cluster_map(smem_u32(&full[s]), 0);
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * R::kStage);
-                    tma_load_2d_pair(p, &xmap, bar, c * kChunkK, t);
-                    tma_load_2d_pair(p + kXBytes, w, bar, c * kChunkK, row);
+#pragma unroll
+                    for (int j = 0; j < R::kPer; ++j) {         // past the last column: zeros
+                        tma_load_2d_pair(p + j * R::kChunk, &xmap, bar, (c + j) * kChunkK, t);
+                        tma_load_2d_pair(p + j * R::kChunk + kXBytes, w, bar, (c + j) * kChunkK, row);
+                    }
                 }
                 __syncwarp();
                 if (++s == kStages) { s = 0; lap ^= 1; }
@@ -230,8 +238,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             const uint64_t wdesc = make_sdesc(smem_u32(ring) + kXBytes, 16u, 1024u, kLayoutSw128);
             bool stop = false;
             for (int64_t i = pair; i < a.tiles && !stop; i += pairs) {
-                int left = 0;           // chunks until the next accumulator
-                for (int c = 0; c < a.chunks; ++c) {
+                int left = 0;           // stages until the next accumulator
+                for (int c = 0; c < a.chunks; c += R::kPer) {
                     const bool fresh = left == 0;
                     if (fresh) {
                         if (!mbar_wait_warp(&accempty[use & 1], ((use >> 1) & 1) ^ 1u, &abort_flag)) {
@@ -239,7 +247,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                             break;
                         }
                         tc_fence_after();
-                        left = kF32 ? min(a.part, a.chunks - c) : a.chunks;
+                        left = (min(kF32 ? a.part : a.chunks, a.chunks - c) + R::kPer - 1) / R::kPer;
                     }
                     if (!mbar_wait_warp(&full[s], lap, &abort_flag)) {
                         stop = true;
@@ -250,9 +258,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                         const uint32_t d = tmem + (use & 1) * kCols;
                         const uint64_t at = (uint64_t)(s * (int)(R::kStage >> 4));
 #pragma unroll
-                        for (int kk = 0; kk < kChunkK / 16; ++kk)
-                            tc_mma_bf16_pair(d, xdesc + at + kk * 2, wdesc + at + kk * 2, idesc,
-                                             fresh && kk == 0 ? 0u : 1u);
+                        for (int j = 0; j < R::kPer; ++j)
+#pragma unroll
+                            for (int kk = 0; kk < kChunkK / 16; ++kk) {
+                                const uint64_t off = at + (uint64_t)(j * (R::kChunk >> 4) + kk * 2);
+                                tc_mma_bf16_pair(d, xdesc + off, wdesc + off, idesc, fresh && j + kk == 0 ? 0u : 1u);
+                            }
                         tc_commit_pair(&empty[s]);
                         if (left == 0) tc_commit_pair(&accfull[use & 1]);
                     }
@@ -387,21 +398,36 @@ int launch_tiles(ProjectCall& c, int pairs)
 
 }  // namespace
 
+namespace {
+
+// Rounds that the device's pairs take for the tiles of so many columns.
+int64_t rounds_of(const ProjectCall& c, int cols)
+{
+    const int pairs = std::max(1, device_sms() / 2), out = c.W_up ? cols / 2 : cols;
+    return ((c.a.T + kPairTokens - 1) / kPairTokens * ((c.a.N + out - 1) / out) + pairs - 1) / pairs;
+}
+
+// A chunk of a narrow tile takes 0.65 of a wide one's time: narrow tiles where
+// the last round of wide ones would leave many pairs idle (512 tokens, 4096 ->
+// 4096: 18.0 us narrow, 25.4 wide; 768: 29.4 and 28.1).  The fp32 form keeps 64
+// sums per lane beside the epilogue's own values; 128 would not fit.
+bool wide_tiles(const ProjectCall& c) { return !c.a.y_f32 && rounds_of(c, 256) <= 0.65 * rounds_of(c, 128); }
+
+}  // namespace
+
+double project_tile_cost(const ProjectCall& c)
+{
+    const bool wide = wide_tiles(c);
+    const double rounds = (double)rounds_of(c, wide ? 256 : 128);
+    return rounds * c.a.chunks * (wide ? 545. : 355.) + 9500 + (c.W_up ? rounds * 3500 : 0);
+}
+
 int launch_project_tile(ProjectCall& c)
 {
     const int pairs = device_sms() / 2;
-    const bool gated = c.W_up != nullptr;
+    const bool gated = c.W_up != nullptr, wide = wide_tiles(c);
     if (c.a.T > 0x7fffffff - kPairTokens) return ADAFUSE_ERR_UNSUPPORTED;
-    // Wide tiles feed the tensor core best; narrow ones where the last round
-    // of wide tiles would leave many pairs idle.
-    const int64_t m = (c.a.T + kPairTokens - 1) / kPairTokens;
-    const auto rounds = [&](int cols) {
-        const int out = gated ? cols / 2 : cols;
-        return (m * ((c.a.N + out - 1) / out) + pairs - 1) / pairs;
-    };
-    const bool wide = rounds(256) <= 0.68 * rounds(128);
     if (gated) return wide ? launch_tiles<256, true, false>(c, pairs) : launch_tiles<128, true, false>(c, pairs);
-    // 64 sums per lane beside the epilogue's own values; 128 would not fit the registers
     if (c.a.y_f32) return launch_tiles<128, false, true>(c, pairs);
     return wide ? launch_tiles<256, false, false>(c, pairs) : launch_tiles<128, false, false>(c, pairs);
 }

@@ -434,12 +434,13 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank)
     return r;
 }
 
-__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr)
+// Copies this CTA's shared memory into another's of the cluster and counts the
+// bytes on a barrier there (16-byte aligned addresses and size; `dst` and `bar`
+// are shared::cluster addresses of the same CTA).
+__device__ __forceinline__ void bulk_copy_cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar)
 {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    return v;
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "r"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
 // ------------------------------------------------------------------ CTA pairs
