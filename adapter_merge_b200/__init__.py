@@ -1,5 +1,7 @@
 """Python binding of libadafuse.so (the AdaFuse fused gated multi-LoRA path on
-B200).  Argument marshalling only: every step of the path runs in the CUDA
+B200).  Argument marshalling only (through ctypes; for the operators between
+the adapted linears, which run once per layer and token, through the extension
+module _binding): every step of the path runs in the CUDA
 kernels behind the C ABI declared in include/adafuse.h.  PyTorch supplies
 device memory and streams.  There is no fallback: if the shared library is
 missing or fails to load, importing the binding's entry points raises.
@@ -8,7 +10,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from typing import Optional, Sequence
 
 __all__ = [
@@ -19,6 +20,7 @@ __all__ = [
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libadafuse.so")
+_BINDING_PATH = os.path.join(_HERE, "_binding.so")
 
 OK = 0
 ERR_INVALID_ARG = 1
@@ -77,6 +79,7 @@ class Heads(ctypes.Structure):
 
 
 _lib = None
+_native = None
 
 
 def library_path() -> str:
@@ -185,33 +188,27 @@ def round_bf16(src, out=None, stream=None):
 # ---------------------------------------------------------------- operators
 # The operators between the adapted linears.  Each runs on its tensors' device
 # and, unless `stream` is given, on that device's current stream; a result that
-# the call allocates belongs to the stream it is computed on.  A decode step
-# makes these calls for one token, so the checks ask each tensor once.
+# the call allocates belongs to the stream it is computed on.  The arguments
+# are checked and passed on by the extension module _binding: bad tensors raise
+# ValueError, the library's error codes AdafuseError.
 
-def _rows(name: str, t, dtype, shape, dev: int) -> int:
-    """Checks a [rows, n] operand with unit stride along its rows; returns its row stride."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}; expected {dtype} {tuple(shape)}"
-                         f"{'' if dev < 0 else f' on cuda:{dev}'}")
-    rows, inner = t.stride()
-    if inner != 1 and shape[1] > 1:
-        raise ValueError(f"{name}: the elements of a row must be adjacent (strides {t.stride()})")
-    return rows
+def _operators():
+    """The extension module, with the library's entry points installed."""
+    global _native
+    if _native is None:
+        import importlib.util
 
-
-def _vector(name: str, t, dtype, n: int, dev: int):
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != (n,) or t.get_device() != dev or (t.stride(0) != 1 and n > 1):
-        raise ValueError(f"{name}: expected {n} adjacent elements of {dtype} on the call's device, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _matrix(name: str, t):
-    if t.dim() != 2:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected two dimensions")
-    return t.shape
+        import torch  # noqa: F401  (its libraries, which the module links)
+        L = lib()
+        if not os.path.exists(_BINDING_PATH):
+            raise RuntimeError(f"_binding.so not built ({_BINDING_PATH}); run adapter_merge_b200.build.build()")
+        spec = importlib.util.spec_from_file_location(__name__ + "._binding", _BINDING_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.install(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.adafuse_project, L.adafuse_gated_project, L.adafuse_epilogue, L.adafuse_rotary)))
+        _native = module
+    return _native
 
 
 def _activation(name) -> int:
@@ -221,42 +218,8 @@ def _activation(name) -> int:
         raise ValueError(f"activation {name!r} is none of {[a for a in ACTIVATIONS if a]}") from None
 
 
-def _result_type(out, out_dtype):
-    import torch
-    kind = out.dtype if out is not None else out_dtype or torch.bfloat16
-    if kind not in (torch.bfloat16, torch.float32) or (out_dtype is not None and kind != out_dtype):
-        raise ValueError("the result is bfloat16 or float32")
-    return kind
-
-
-def _on(dev: int, stream):
-    """(raw stream, context): the stream a call on device `dev` goes to, and,
-    where device or stream are not the current ones, a context that makes them
-    so for what the call allocates (else None)."""
-    import torch
-    if dev < 0:
-        raise ValueError("expected CUDA tensors")
-    if stream is None:
-        if dev == torch.cuda.current_device():
-            return torch._C._cuda_getCurrentRawStream(dev), None
-        return torch._C._cuda_getCurrentRawStream(dev), torch.cuda.device(dev)
-    raw = stream if isinstance(stream, int) else stream.cuda_stream
-    device = torch.device("cuda", dev)
-    return raw, torch.cuda.stream(torch.cuda.ExternalStream(raw, device=device) if raw
-                                  else torch.cuda.default_stream(device))
-
-
-def _call(name: str, ctx, like, T: int, n: int, kind, out, args):
-    """One library call, args(pointer of out); allocates `out` [T, n] beside `like` if None."""
-    if ctx is not None:
-        with ctx:
-            return _call(name, None, like, T, n, kind, out, args)
-    if out is None:
-        out = like.new_empty(T, n) if like.dtype is kind else like.new_empty(T, n, dtype=kind)
-    rc = args(out.data_ptr())
-    if rc:
-        _check(rc, name)
-    return out
+def _raw(stream):
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def project(x, W, bias=None, activation=None, residual=None, out=None, out_dtype=None, status=None, stream=None):
@@ -267,22 +230,11 @@ def project(x, W, bias=None, activation=None, residual=None, out=None, out_dtype
     Returns `out`, bf16 [T, d_out]; out_dtype=torch.float32 leaves the fp32
     result unrounded (a row-parallel rank's partial sums).  STATUS_TIMEOUT is
     OR-ed into `status` (int32 [1]) when a device-side wait gave up."""
-    import torch
-    bf16, dev = torch.bfloat16, x.get_device()
-    (T, K), N = _matrix("x", x), _matrix("W", W)[0]
-    ldx, ldw = _rows("x", x, bf16, (T, K), dev), _rows("W", W, bf16, (N, K), dev)
-    kind = bf16 if out is None and out_dtype is None else _result_type(out, out_dtype)
-    b = None if bias is None else _vector("bias", bias, bf16, N, dev)
-    r = ldr = ldy = None
-    if residual is not None:
-        r, ldr = residual.data_ptr(), _rows("residual", residual, bf16, (T, N), dev)
-    if out is not None:
-        ldy = _rows("out", out, kind, (T, N), dev)
-    s = None if status is None else _vector("status", status, torch.int32, 1, dev)
-    flags = _activation(activation) | (0 if kind is bf16 else OUT_F32)
-    raw, ctx = _on(dev, stream)
-    return _call("adafuse_project", ctx, x, T, N, kind, out, lambda y: lib().adafuse_project(
-        x.data_ptr(), T, K, ldx, W.data_ptr(), N, ldw, b, r, ldr or 0, y, N if ldy is None else ldy, flags, s, raw))
+    r = (_native or _operators()).project(x, W, bias, _activation(activation), residual, out, out_dtype, status,
+                                          _raw(stream))
+    if r.__class__ is int:
+        raise AdafuseError(r, "adafuse_project")
+    return r if out is None else out
 
 
 def gated_project(x, W_gate, W_up, bias_gate=None, bias_up=None, activation="silu", out=None, status=None,
@@ -290,19 +242,11 @@ def gated_project(x, W_gate, W_up, bias_gate=None, bias_up=None, activation="sil
     """act(x W_gate^T + bias_gate) * (x W_up^T + bias_up) in one launch: the
     feed-forward block's two projections, activation and product.  Weights bf16
     [d_out, d_in] with the same row stride; everything else as project."""
-    import torch
-    bf16, dev = torch.bfloat16, x.get_device()
-    (T, K), N = _matrix("x", x), _matrix("W_gate", W_gate)[0]
-    ldx, ldw = _rows("x", x, bf16, (T, K), dev), _rows("W_gate", W_gate, bf16, (N, K), dev)
-    if _rows("W_up", W_up, bf16, (N, K), dev) != ldw and N > 1:
-        raise ValueError("W_gate and W_up need the same row stride")
-    bg, bu = _vector("bias_gate", bias_gate, bf16, N, dev), _vector("bias_up", bias_up, bf16, N, dev)
-    ldy = N if out is None else _rows("out", out, bf16, (T, N), dev)
-    s = None if status is None else _vector("status", status, torch.int32, 1, dev)
-    flags = _activation(activation)
-    raw, ctx = _on(dev, stream)
-    return _call("adafuse_gated_project", ctx, x, T, N, bf16, out, lambda y: lib().adafuse_gated_project(
-        x.data_ptr(), T, K, ldx, W_gate.data_ptr(), W_up.data_ptr(), N, ldw, bg, bu, y, ldy, flags, s, raw))
+    r = (_native or _operators()).gated_project(x, W_gate, W_up, bias_gate, bias_up, _activation(activation), out,
+                                                status, _raw(stream))
+    if r.__class__ is int:
+        raise AdafuseError(r, "adafuse_gated_project")
+    return r if out is None else out
 
 
 def epilogue(y, bias=None, activation=None, up=None, residual=None, out=None, out_dtype=None, stream=None):
@@ -312,24 +256,11 @@ def epilogue(y, bias=None, activation=None, up=None, residual=None, out=None, ou
     [T, n], both bf16 or both fp32; bias bf16 [n]; residual bf16 [T, n].  Rows
     may be strided, those of y, up and residual one expanded row.  Returns
     `out`, bf16 [T, n] (or fp32); it may be y, up or residual itself."""
-    import torch
-    bf16, f32, dev = torch.bfloat16, torch.float32, y.get_device()
-    T, n = shape = _matrix("y", y)
-    given = f32 if y.dtype is f32 else bf16
-    ldy = _rows("y", y, given, shape, dev)
-    kind = bf16 if out is None and out_dtype is None else _result_type(out, out_dtype)
-    b = None if bias is None else _vector("bias", bias, bf16, n, dev)
-    u = r = None
-    ldu = ldr = 0
-    if up is not None:
-        u, ldu = up.data_ptr(), _rows("up", up, given, shape, dev)
-    if residual is not None:
-        r, ldr = residual.data_ptr(), _rows("residual", residual, bf16, shape, dev)
-    ldo = n if out is None else _rows("out", out, kind, shape, dev)
-    flags = _activation(activation) | (IN_F32 if given is f32 else 0) | (OUT_F32 if kind is f32 else 0)
-    raw, ctx = _on(dev, stream)
-    return _call("adafuse_epilogue", ctx, y, T, n, kind, out, lambda o: lib().adafuse_epilogue(
-        y.data_ptr(), T, n, ldy, b, u, ldu, r, ldr, o, ldo, flags, raw))
+    r = (_native or _operators()).epilogue(y, bias, _activation(activation), up, residual, out, out_dtype,
+                                           _raw(stream))
+    if r.__class__ is int:
+        raise AdafuseError(r, "adafuse_epilogue")
+    return r if out is None else out
 
 
 def rotary_frequencies(dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
@@ -374,24 +305,6 @@ def rotary_frequencies(dim: int, base: float = 10000.0, scaling: Optional[str] =
     return freq.to(device) if device is not None else freq, mult
 
 
-_HEADS = struct.Struct("@PPqqqqPi4x")       # adafuse_heads
-
-
-def _heads(name: str, t, out, weight, shape, dev: int) -> bytes:
-    import torch
-    bf16 = torch.bfloat16
-    if t.dtype is not bf16 or out.dtype is not bf16 or t.shape != shape or out.shape != shape or \
-            t.get_device() != dev or out.get_device() != dev:
-        raise ValueError(f"{name}, {name}_out: expected {bf16} {tuple(shape)} on the call's device, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device} and {out.dtype} {tuple(out.shape)} on {out.device}")
-    its, ihs, i1 = t.stride()
-    ots, ohs, o1 = out.stride()
-    if (i1 != 1 or o1 != 1) and shape[2] > 1:
-        raise ValueError(f"{name}: the elements of a head must be adjacent (strides {t.stride()}, {out.stride()})")
-    w = 0 if weight is None else _vector(name + "_weight", weight, bf16, shape[2], dev)
-    return _HEADS.pack(t.data_ptr(), out.data_ptr(), its, ihs, ots, ohs, w, shape[1])
-
-
 def rotary(q, k, positions, freq, layout: str = "half", factor: float = 1.0, q_weight=None, k_weight=None,
            eps: float = 1e-6, q_out=None, k_out=None, stream=None):
     """Rotates queries and keys by their positions, after an RMS norm of each
@@ -402,44 +315,13 @@ def rotary(q, k, positions, freq, layout: str = "half", factor: float = 1.0, q_w
     i + rot/2, "interleaved" 2i and 2i + 1; `factor` scales the rotated
     elements.  q_weight / k_weight bf16 [D].  Returns (q_out, k_out), new
     contiguous tensors unless given; q_out may be q itself, k_out k."""
-    import torch
-    dev = q.get_device()
-    if q.dim() != 3 or (k is not None and k.dim() != 3):
-        raise ValueError("q and k have three dimensions: tokens, heads, elements")
-    T, Hq, D = shape = q.shape
-    flags = 0
-    if layout != "half":
-        if layout != "interleaved":
-            raise ValueError(f"layout {layout!r} is neither 'half' nor 'interleaved'")
-        flags = PAIRS
-    kind = torch.int64
-    if positions.dtype is torch.int32:
-        kind = torch.int32
-        flags |= POS_I32
-    p = _vector("positions", positions, kind, T, dev)
-    if freq.dim() != 1:
-        raise ValueError("freq has one dimension")
-    n = freq.shape[0]
-    f = _vector("freq", freq, torch.float64, n, dev)
-    if k is None and (k_weight is not None or k_out is not None):
-        raise ValueError("k_weight and k_out go with k")
-    raw, ctx = _on(dev, stream)
-    if ctx is not None:
-        with ctx:
-            return rotary(q, k, positions, freq, layout, factor, q_weight, k_weight, eps, q_out, k_out)
-    if q_out is None:
-        q_out = q.new_empty(T, Hq, D)
-    hk = None
-    if k is not None:
-        Hk = k.shape[1]
-        if k_out is None:
-            k_out = k.new_empty(T, Hk, D)
-        hk = _heads("k", k, k_out, k_weight, (T, Hk, D), dev)
-    rc = lib().adafuse_rotary(_heads("q", q, q_out, q_weight, shape, dev), hk, T, D, 2 * n, p, f, factor, eps,
-                              flags, raw)
-    if rc:
-        _check(rc, "adafuse_rotary")
-    return q_out, k_out
+    if layout not in ("half", "interleaved"):
+        raise ValueError(f"layout {layout!r} is neither 'half' nor 'interleaved'")
+    r = (_native or _operators()).rotary(q, k, positions, freq, 0 if layout == "half" else PAIRS, factor, q_weight,
+                                         k_weight, eps, q_out, k_out, _raw(stream))
+    if r.__class__ is int:
+        raise AdafuseError(r, "adafuse_rotary")
+    return r[0] if q_out is None else q_out, r[1] if k_out is None else k_out
 
 
 class Plan:

@@ -1,4 +1,5 @@
-"""Build libadafuse.so in-tree with nvcc for sm_100a (no GPU needed)."""
+"""Build libadafuse.so in-tree with nvcc for sm_100a (no GPU needed), and the
+Python binding of the operators with the host compiler."""
 from __future__ import annotations
 
 import glob
@@ -8,6 +9,7 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libadafuse.so")
+BINDING = os.path.join(HERE, "_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [
@@ -28,14 +30,39 @@ def headers():
             + [os.path.join(os.path.dirname(HERE), "include", "adafuse.h")])
 
 
+def newer_than(target: str, files) -> bool:
+    """Whether `target` exists and none of the files was changed after it."""
+    return os.path.exists(target) and all(os.path.getmtime(f) <= os.path.getmtime(target) for f in files)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in sources() + headers())
+    return newer_than(LIB, sources() + headers())
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    source = os.path.join(CSRC, "binding.cpp")
+    inc = os.path.join(os.path.dirname(HERE), "include")
+    if not force and newer_than(BINDING, [source, os.path.join(inc, "adafuse.h")]):
+        return BINDING
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    dirs = [inc, sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+            os.path.join(root, "include")]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f for d in dirs for f in ("-I", d)),
+           source, "-o", tmp, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.check_call(cmd)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    build_binding(force, verbose)
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
