@@ -16,8 +16,8 @@
 // an item is a vector of V elements together with the vector of its partners
 // (one vector that holds both in the interleaved layout, one unrotated vector
 // past `rot`), and 2^n lanes share a head, one item each, so that the norm's
-// sum is a shuffle among them.  A lane loads the items of two heads (of four,
-// interleaved) before it rotates them.  No barrier across warps.
+// sum is a shuffle among them.  A lane loads its next heads' items before it
+// rotates those it has.  No barrier across warps.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -28,7 +28,10 @@ namespace {
 
 constexpr int kRotThreads = 128;
 constexpr int kRotWarps = kRotThreads / 32;
-constexpr int kFlight = 2;              // heads per lane in flight (four vectors)
+// Heads that a lane loads ahead of those it rotates.  8192 tokens of 32 + 8
+// heads of 128 with norms: 33.3 us with two, 36.9 with one; 4097 tokens of 80
+// heads, interleaved: 30.7 with two (of one vector each).
+__host__ __device__ constexpr int flight(bool pairs, bool norm) { return (norm ? 2 : 1) * (pairs ? 2 : 1); }
 constexpr int kLaneHeads = 20;          // most heads of a prompt's token per lane
 constexpr int kMaxHeadDim = 1024;
 
@@ -153,83 +156,162 @@ __device__ __forceinline__ void turn_token(const RotArgs& a, int64_t t, float* c
     __syncwarp();
 }
 
+// Two fp32 values and the arithmetic on both at once.
+struct Two {
+    uint64_t v;
+    __device__ __forceinline__ Two() {}
+    __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ float2 get() const
+    {
+        float2 r;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+        return r;
+    }
+};
+__device__ __forceinline__ Two operator*(Two a, Two b)
+{
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c)
+{
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ Two unpack2(uint32_t w) { return Two(bf16lo(w), bf16hi(w)); }
+__device__ __forceinline__ uint32_t pack2(Two a)
+{
+    const float2 f = a.get();
+    return pack_bf16x2(f.x, f.y);
+}
+
+template <int V>
+__device__ __forceinline__ void store_raw(const Raw<V>& r, uint16_t* p)
+{
+    if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    else *reinterpret_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
+}
+
 // The heads of one kind of a token, whose items (j of every head) one lane
 // holds: heads h0, h0 + stride, ...; the same number of steps for all lanes.
-// The coefficients of a pair (p, q) -> (p a - q b, p c + q d) hold the
-// weights, so a norm costs its sum and one factor more.
+// A pair turns as (p, q) -> (p a - q b, p c + q d); the coefficients hold the
+// weights, so a norm costs its sum and one factor more.  All arithmetic is on
+// two neighbouring elements at a time: two pairs, or, interleaved, the two
+// elements of one.
 template <int V, bool kPairs, bool kNorm>
 __device__ __forceinline__ void rotate_heads(const RotArgs& a, const Heads& m, int n, int64_t t, int h0, int stride,
                                              int group, const Item<V>& it, bool mine, const float* cosv,
                                              const float* sinv)
 {
-    constexpr int P = kPairs ? V / 2 : V;           // pairs of an item
-    constexpr int F = kPairs ? 2 * kFlight : kFlight;
+    constexpr int H = V / 2;                        // words of a vector
+    constexpr int F = flight(kPairs, kNorm);
     const bool turns = it.pair >= 0, two = !kPairs && it.o2 >= 0;
-    float ca[P], cb[P], cc[P], cd[P];
+    // half: first' = first A - second B, second' = first C + second D, of two pairs
+    // interleaved: (p', q') = (p, q) A + (q, p) B, of one pair
+    Two A[H], B[H], C[H], D[H];
     if (mine) {
-        Vec<V> w0, w1;
+        Raw<V> w0, w1;
+#pragma unroll
+        for (int i = 0; i < H; ++i) w0.w[i] = w1.w[i] = 0x3f803f80u;        // ones
         if constexpr (kNorm) {
             w0.load(m.weight + it.o1);
             if (two) w1.load(m.weight + it.o2);
         }
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const float c = turns ? cosv[it.pair + i] : 1.f, s = turns ? sinv[it.pair + i] : 0.f;
-            const float wp = !kNorm ? 1.f : kPairs ? w0.v[2 * i] : w0.v[i];
-            const float wq = !kNorm ? 1.f : kPairs ? w0.v[2 * i + 1] : turns ? w1.v[i] : 0.f;
-            ca[i] = c * wp;
-            cb[i] = s * wq;
-            cc[i] = s * wp;
-            cd[i] = c * wq;
+        for (int i = 0; i < H; ++i) {
+            const float p0 = bf16lo(w0.w[i]), p1 = bf16hi(w0.w[i]), q0 = bf16lo(w1.w[i]), q1 = bf16hi(w1.w[i]);
+            if constexpr (kPairs) {
+                const float c = turns ? cosv[it.pair + i] : 1.f, s = turns ? sinv[it.pair + i] : 0.f;
+                A[i] = Two(c * p0, c * p1);
+                B[i] = Two(-s * p1, s * p0);
+            } else {
+                const float c0 = turns ? cosv[it.pair + 2 * i] : 1.f, s0 = turns ? sinv[it.pair + 2 * i] : 0.f;
+                const float c1 = turns ? cosv[it.pair + 2 * i + 1] : 1.f, s1 = turns ? sinv[it.pair + 2 * i + 1] : 0.f;
+                A[i] = Two(c0 * p0, c1 * p1);
+                B[i] = Two(-s0 * q0, -s1 * q1);
+                C[i] = Two(s0 * p0, s1 * p1);
+                D[i] = Two(c0 * q0, c1 * q1);
+            }
         }
     }
     const uint16_t* in = m.in + t * m.its + h0 * m.ihs;
     uint16_t* out = m.out + t * m.ots + h0 * m.ohs;
     const int64_t din = stride * m.ihs, dout = stride * m.ohs;
+    Raw<V> nx[F], ny[F];
+    const auto fetch = [&](int h) {
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+            if (mine && h + j * stride < n) {
+                nx[j].load(in + it.o1);
+                if (two) ny[j].load(in + it.o2);
+            }
+            in += din;
+        }
+    };
+    fetch(h0);
     for (int h = h0; h - group < n; h += F * stride) {
         Raw<V> rx[F], ry[F];
 #pragma unroll
         for (int j = 0; j < F; ++j) {
-            if (mine && h + j * stride < n) {
-                rx[j].load(in + it.o1);
-                if (two) ry[j].load(in + it.o2);
-            }
-            in += din;
+            rx[j] = nx[j];
+            ry[j] = ny[j];
         }
+        fetch(h + F * stride);
 #pragma unroll
         for (int j = 0; j < F; ++j) {
             const bool live = mine && h + j * stride < n;
-            Vec<V> x, y;
-            x.from(rx[j]);
-            if constexpr (!kPairs) y.from(ry[j]);
-            float r = 1.f;
+            Two r(1.f, 1.f);
             if constexpr (kNorm) {
-                float sum = live ? x.squares() : 0.f;
-                if (live && two) sum += y.squares();
+                float sum = 0.f;
+                if (live) {
+                    Two s(0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const Two x = unpack2(rx[j].w[i]);
+                        s = fma2(x, x, s);
+                    }
+                    if (two) {
+#pragma unroll
+                        for (int i = 0; i < H; ++i) {
+                            const Two y = unpack2(ry[j].w[i]);
+                            s = fma2(y, y, s);
+                        }
+                    }
+                    const float2 f = s.get();
+                    sum = f.x + f.y;
+                }
                 for (int d = a.lanes / 2; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                r = rsqrtf(sum * a.inv_d + a.eps);
+                const float f = rsqrtf(sum * a.inv_d + a.eps);
+                r = Two(f, f);
             }
             if (live) {
+                if (turns) {
 #pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    float& p = kPairs ? x.v[2 * i] : x.v[i];
-                    float& q = kPairs ? x.v[2 * i + 1] : y.v[i];
-                    if (turns) {
-                        const float u = p * ca[i] - q * cb[i];
-                        q = p * cc[i] + q * cd[i];
-                        p = u;
-                    } else if (kNorm) {
-                        p *= ca[i];
-                        if (kPairs) q *= cd[i];
+                    for (int i = 0; i < H; ++i) {
+                        const Two x = unpack2(rx[j].w[i]);
+                        if constexpr (kPairs) {
+                            Two u = fma2(Two(bf16hi(rx[j].w[i]), bf16lo(rx[j].w[i])), B[i], x * A[i]);
+                            if (kNorm) u = u * r;
+                            rx[j].w[i] = pack2(u);
+                        } else {
+                            const Two y = unpack2(ry[j].w[i]);
+                            Two u = fma2(y, B[i], x * A[i]), v = fma2(y, D[i], x * C[i]);
+                            if (kNorm) {
+                                u = u * r;
+                                v = v * r;
+                            }
+                            rx[j].w[i] = pack2(u);
+                            ry[j].w[i] = pack2(v);
+                        }
                     }
-                    if (kNorm) {
-                        p *= r;
-                        if (kPairs || two) q *= r;
-                    }
+                } else if constexpr (kNorm) {
+#pragma unroll
+                    for (int i = 0; i < H; ++i) rx[j].w[i] = pack2(unpack2(rx[j].w[i]) * A[i] * r);
                 }
-                x.store(out + it.o1);
-                if constexpr (!kPairs)
-                    if (two) y.store(out + it.o2);
+                store_raw(rx[j], out + it.o1);
+                if (two) store_raw(ry[j], out + it.o2);
             }
             out += dout;
         }

@@ -88,20 +88,28 @@ def plan_flags(kind: str) -> int:
     raise ValueError(kind)
 
 
-def reduce_output(kind: str, y, out=None, group=None):
+def reduce_output(kind: str, y, out=None, group=None, bias=None, residual=None):
     """Complete a rank's apply output.  Column-parallel: y (bf16) is already
     final, the rank's block of output columns.  Row-parallel: y is the rank's
-    fp32 partial (PLAN_Y_F32); it is all-reduced (sum, in place), and if `out`
-    is given (a bf16 device tensor of y's shape) the sum is rounded once into
-    it by the library and `out` is returned, else the summed partial.  Every
-    rank must call this in the same order."""
+    fp32 partial (PLAN_Y_F32, or a projection with out_dtype=torch.float32); it
+    is all-reduced (sum, in place), and if `out` is given (a bf16 device tensor
+    of y's shape) the sum is rounded once into it by the library and `out` is
+    returned, else the summed partial.  A bias [d_out] or a residual [T, d_out]
+    (bf16; the residual may be `out`) is added to the sum before that one
+    rounding, into a new bf16 tensor if `out` is None.  Every rank must call
+    this in the same order."""
     if kind == COLUMN:
+        if bias is not None or residual is not None:
+            raise ValueError("a bias or residual is added to row-parallel sums; a column-parallel block is final")
         return y
     if kind != ROW:
         raise ValueError(kind)
     import torch.distributed as dist
     if dist.is_initialized() and dist.get_world_size(group) > 1:
         dist.all_reduce(y, op=dist.ReduceOp.SUM, group=group)
+    if bias is not None or residual is not None:
+        from adapter_merge_b200 import epilogue
+        return epilogue(y, bias=bias, residual=residual, out=out)
     if out is None:
         return y
     from adapter_merge_b200 import round_bf16

@@ -523,6 +523,26 @@ def test_a_wait_that_gives_up_is_reported(am):
         assert torch.equal(again, good) and int(status) == 0
 
 
+def test_row_parallel_shards_of_a_projection(am):
+    """Two shards of the input columns, fp32 partial sums, added (in place of
+    the all-reduce), then bias and residual with the one rounding."""
+    from adapter_merge_b200 import tp
+    T, K, N = 37, 512, 264
+    x, W, b, r = rnd(T, K), rnd(N, K, seed=1, std=0.05), rnd(N, seed=2), rnd(T, N, seed=3)
+    parts = []
+    for rank in range(2):
+        i0, i1 = tp.block(K, rank, 2)
+        parts.append(am.project(x[:, i0:i1], W[:, i0:i1], out_dtype=F32))
+    y = parts[0] + parts[1]
+    v, e = product64(x, W, None, 512)
+    want = v + b.to(F64) + r.to(F64)
+    err = e + 4 * STEP * (v.abs() + b.to(F64).abs() + r.to(F64).abs())
+    check(tp.reduce_output(tp.ROW, y, bias=b, residual=r), want, err)
+    assert tp.reduce_output(tp.ROW, y, out=r, bias=b, residual=r) is r
+    check(r, want, err)
+    check(tp.reduce_output(tp.ROW, y, out=r), v, err)
+
+
 # ------------------------------------------------------------------ a layer
 
 def test_a_layer_merged_and_unmerged(am, cuda_device):

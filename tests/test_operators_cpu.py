@@ -175,3 +175,12 @@ def test_binding_refusals(am):
         with pytest.raises(ValueError):
             call()
             pytest.fail(f"call {i} was accepted")
+
+
+def test_reduce_output_adds_to_row_parallel_sums_only():
+    from adapter_merge_b200 import tp
+    y, b = torch.zeros(2, 8), torch.zeros(8, dtype=BF16)
+    assert tp.reduce_output(tp.COLUMN, y) is y and tp.reduce_output(tp.ROW, y) is y
+    for kw in ({"bias": b}, {"residual": y.to(BF16)}):
+        with pytest.raises(ValueError):
+            tp.reduce_output(tp.COLUMN, y, **kw)
