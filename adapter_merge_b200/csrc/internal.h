@@ -102,7 +102,8 @@ inline bool rows_overlap(RowSpan a, RowSpan b)
     if (b.pitch == 0) b.rows = 1;
     if (a.rows < 1 || b.rows < 1) return false;
     const int64_t pa = reinterpret_cast<int64_t>(a.base), pb = reinterpret_cast<int64_t>(b.base);
-    const int64_t ea = pa + (a.rows - 1) * a.pitch + a.row_bytes, eb = pb + (b.rows - 1) * b.pitch + b.row_bytes;
+    const __int128 ea = (__int128)(a.rows - 1) * a.pitch + pa + a.row_bytes;
+    const __int128 eb = (__int128)(b.rows - 1) * b.pitch + pb + b.row_bytes;
     if (ea <= pb || eb <= pa) return false;
     if (a.rows == 1 && b.rows == 1) return true;
     const int64_t pitch = a.rows == 1 ? b.pitch : a.pitch;
@@ -111,6 +112,10 @@ inline bool rows_overlap(RowSpan a, RowSpan b)
     const int64_t d = ((pb - pa) % pitch + pitch) % pitch;     // b's first byte within a's pitch
     return d < a.row_bytes || d + b.row_bytes > pitch;
 }
+
+// Strides that the operators take, in elements; their byte offsets fit 64 bits
+// with any number of rows that memory holds.
+inline bool plain_stride(int64_t ld) { return ld >= 0 && ld < (1ll << 38); }
 
 inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 

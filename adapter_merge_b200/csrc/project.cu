@@ -451,7 +451,7 @@ int check(ProjectCall& c, const void* bias, const void* bias_up, bool gated, uin
     const uint32_t act = flags & ADAFUSE_ACT_MASK;
     if (flags & ~(ADAFUSE_ACT_MASK | ADAFUSE_TEST_STALL | (gated ? 0u : ADAFUSE_OUT_F32))) return ADAFUSE_ERR_INVALID_ARG;
     if (a.T < 0 || c.K < 1 || a.N < 1) return ADAFUSE_ERR_INVALID_ARG;
-    if (act > ADAFUSE_ACT_GELU_TANH || c.K % 8 || a.N % 8 || a.T > 0x7fffffff) return ADAFUSE_ERR_UNSUPPORTED;
+    if (act > ADAFUSE_ACT_GELU_TANH || c.K % 8 || a.N % 8 || a.T > 0x7fffff00) return ADAFUSE_ERR_UNSUPPORTED;
     if (a.T == 0) return ADAFUSE_OK;
     if (!c.x || !c.W || !a.y || (gated && !c.W_up)) return ADAFUSE_ERR_INVALID_ARG;
     a.y_f32 = flags & ADAFUSE_OUT_F32 ? 1 : 0;
@@ -463,7 +463,8 @@ int check(ProjectCall& c, const void* bias, const void* bias_up, bool gated, uin
     for (const void* p : {c.x, c.W, c.W_up, (const void*)a.y, (const void*)a.residual, bias, bias_up})
         if (!aligned_to(p, 16)) return ADAFUSE_ERR_UNSUPPORTED;
     if (c.ldx % 8 || c.ldw % 8 || a.ldr % 8 || a.ldy % (a.y_f32 ? 4 : 8)) return ADAFUSE_ERR_UNSUPPORTED;
-    if (c.ldx >= (1ll << 38) || c.ldw >= (1ll << 38)) return ADAFUSE_ERR_UNSUPPORTED;      // tensor-map strides
+    for (const int64_t ld : {c.ldx, c.ldw, a.ldr, a.ldy})
+        if (!plain_stride(ld)) return ADAFUSE_ERR_UNSUPPORTED;
     const RowSpan y{a.y, a.T, a.N * size, a.ldy * size};
     const RowSpan in[] = {{c.x, a.T, 2ll * c.K, 2 * c.ldx}, {c.W, a.N, 2ll * c.K, 2 * c.ldw},
                           {c.W_up, a.N, 2ll * c.K, 2 * c.ldw}, {bias, 1, 2ll * a.N, 2ll * a.N},

@@ -429,7 +429,6 @@ int launch_project_tile(ProjectCall& c)
 {
     const int pairs = device_sms() / 2;
     const bool gated = c.W_up != nullptr, wide = wide_tiles(c);
-    if (c.a.T > 0x7fffffff - kPairTokens) return ADAFUSE_ERR_UNSUPPORTED;
     if (gated) return wide ? launch_tiles<256, true, false>(c, pairs) : launch_tiles<128, true, false>(c, pairs);
     if (c.a.y_f32) return launch_tiles<128, false, true>(c, pairs);
     return wide ? launch_tiles<256, false, false>(c, pairs) : launch_tiles<128, false, false>(c, pairs);

@@ -447,6 +447,8 @@ int check_heads(const adafuse_heads* m, int64_t T, int32_t D)
     if (!aligned_to(m->in, 2) || !aligned_to(m->out, 2) || !aligned_to(m->weight, 2)) return ADAFUSE_ERR_INVALID_ARG;
     if (m->in_token_stride < 0 || m->in_head_stride < 0 || m->out_token_stride < 0 || m->out_head_stride < 0)
         return ADAFUSE_ERR_INVALID_ARG;
+    for (const int64_t ld : {m->in_token_stride, m->in_head_stride, m->out_token_stride, m->out_head_stride})
+        if (!plain_stride(ld)) return ADAFUSE_ERR_UNSUPPORTED;
     // the outputs of two heads or tokens may not meet: either axis may be the outer one
     const int64_t ts = m->out_token_stride, hs = m->out_head_stride;
     const bool token_outer = (m->heads == 1 || hs >= D) && (T == 1 || ts >= span(1, 0, m->heads, hs, D));
@@ -466,7 +468,7 @@ extern "C" int adafuse_rotary(const adafuse_heads* q, const adafuse_heads* k, in
 {
     if (flags & ~(ADAFUSE_PAIRS | ADAFUSE_POS_I32)) return ADAFUSE_ERR_INVALID_ARG;
     if (!q || T < 0 || head_dim < 1 || rot < 0) return ADAFUSE_ERR_INVALID_ARG;
-    if (rot % 2 || rot > head_dim || head_dim > kMaxHeadDim) return ADAFUSE_ERR_UNSUPPORTED;
+    if (rot % 2 || rot > head_dim || head_dim > kMaxHeadDim || T > 0x7fffffff) return ADAFUSE_ERR_UNSUPPORTED;
     if (T == 0) return ADAFUSE_OK;
     int rc = check_heads(q, T, head_dim);
     if (!rc && k) rc = check_heads(k, T, head_dim);

@@ -346,8 +346,8 @@ ADAFUSE_API int adafuse_round_bf16(const float* in, void* out, int64_t n, adafus
  * 16-byte aligned.
  * Errors: INVALID_ARG (null pointers, T < 0, sizes < 1, unknown flags, a stride
  * shorter than its row with T > 1, overlapping buffers), UNSUPPORTED
- * (alignment, multiples, an activation that is not listed, T over 2^31 - 1),
- * DEVICE, CUDA.
+ * (alignment, multiples, an activation that is not listed, T over 2^31 - 256, a
+ * stride of 2^38 or more), DEVICE, CUDA.
  */
 ADAFUSE_API int adafuse_project(const void* x, int64_t T, int32_t d_in, int64_t x_row_stride, const void* W,
                                 int32_t d_out, int64_t w_row_stride, const void* bias, const void* residual,
@@ -381,7 +381,7 @@ ADAFUSE_API int adafuse_gated_project(const void* x, int64_t T, int32_t d_in, in
  * row for all tokens).  Any n, stride and alignment of whole elements; rows of
  * 16-byte aligned groups of 8 elements move in 16-byte accesses.
  * Errors: INVALID_ARG (as above), UNSUPPORTED (an activation that is not
- * listed, n over 2^31 - 1).
+ * listed, n or T over 2^31 - 1, a stride of 2^38 or more), DEVICE, CUDA.
  */
 ADAFUSE_API int adafuse_epilogue(const void* y, int64_t T, int64_t n, int64_t y_row_stride, const void* bias,
                                  const void* up, int64_t up_row_stride, const void* residual, int64_t r_row_stride,
@@ -417,7 +417,7 @@ typedef struct {
  * may live in one buffer, e.g. rows that hold q, k and v of a token).
  * Errors: INVALID_ARG (null pointers, sizes, unknown flags, overlapping
  * outputs), UNSUPPORTED (rot odd or > head_dim, head_dim > 1024, over 2^16
- * heads), CUDA.
+ * heads, T over 2^31 - 1, a stride of 2^38 or more), DEVICE, CUDA.
  */
 ADAFUSE_API int adafuse_rotary(const adafuse_heads* q, const adafuse_heads* k, int64_t T, int32_t head_dim,
                                int32_t rot, const void* positions, const double* freq, float factor, float eps,

@@ -298,6 +298,32 @@ def test_epilogue_strides_broadcast_and_in_place(am):
         assert got is t[name] and torch.equal(got, want)
 
 
+def test_epilogue_of_one_row_for_all_tokens(am):
+    T, n = 70, 96
+    y, up, r = rnd(1, n), rnd(1, n, seed=1), rnd(1, n, seed=2)
+    got = am.epilogue(y.expand(T, n), activation="relu", up=up.expand(T, n), residual=r.expand(T, n))
+    assert torch.equal(got, am.epilogue(y, activation="relu", up=up, residual=r).expand(T, n))
+
+
+def test_offsets_past_32_bits(am):
+    """5 GB of outputs: rows whose element offsets, and byte offsets, pass 2^31 and 2^32."""
+    T, K, N = 600_000, 64, 4096
+    x, W = rnd(T, K), rnd(N, K, seed=1, std=0.05)
+    y = am.project(x, W)
+    rows = torch.tensor([0, 262_143, 262_144, 524_287, 524_288, T - 257, T - 1], device="cuda")
+    check(y[rows], *product64(x[rows], W, None))
+    z = am.epilogue(y, activation="relu", residual=y, out=y)
+    assert z is y
+    v, e = product64(x[rows], W, None)
+    check(y[rows], act64(v, "relu") + v, 2 * e + 3 * HALF * v.abs())
+    freq, _ = am.rotary_frequencies(64, device="cuda")
+    pos = torch.arange(T, device="cuda")
+    q = y.view(T, 64, 64)
+    want = rotary64(q[rows], None, pos[rows], freq, "half", 1.0, 0)
+    am.rotary(q, None, pos, freq, q_out=q)
+    check(q[rows], *want)
+
+
 def test_epilogue_extremes(am):
     inf, nan = float("inf"), float("nan")
     y = torch.tensor([[0.0, -0.0, inf, nan, 1e4, -1e4, 90.0, -90.0]], device="cuda")

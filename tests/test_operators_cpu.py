@@ -50,6 +50,7 @@ def test_projections_refuse_bad_arguments(am, kw):
 @pytest.mark.parametrize("kw", [
     {"K": 60, "ldx": 60, "ldw": 60}, {"N": 36, "ldy": 36}, {"x": at(0, 8)}, {"W": at(1, 2)}, {"y": at(2, 8)},
     {"ldx": 68}, {"ldw": 70}, {"ldy": 36}, {"flags": 5}, {"flags": 7}, {"T": 1 << 31},
+    {"ldx": 1 << 38}, {"ldw": 1 << 40}, {"ldy": 1 << 60},
 ])
 def test_projections_refuse_what_they_do_not_support(am, kw):
     assert project(am, **kw) == am.ERR_UNSUPPORTED
@@ -93,6 +94,7 @@ def test_epilogue_refusals(am):
         assert epilogue(am, **kw) == bad, kw
     assert epilogue(am, flags=5) == am.ERR_UNSUPPORTED
     assert epilogue(am, n=1 << 31, ldy=1 << 31, ldo=1 << 31) == am.ERR_UNSUPPORTED
+    assert epilogue(am, T=1 << 31) == am.ERR_UNSUPPORTED and epilogue(am, ldo=1 << 38) == am.ERR_UNSUPPORTED
     assert epilogue(am, T=0, y=None, out=None) == am.OK
 
 
@@ -118,7 +120,8 @@ def test_rotary_refusals(am):
                {"out": at(0, 2)}, {"out": at(0), "ots": 48}, {"weight": at(1)}, {"out": at(8)}, {"out": at(9)}):
         assert rotary(am, heads(am, **kw)) == bad, kw
         assert rotary(am, heads(am, src=at(4), out=at(5)), heads(am, **kw)) == bad, kw
-    assert rotary(am, heads(am, n=70000)) == un
+    assert rotary(am, heads(am, n=70000)) == un and rotary(am, ok, T=1 << 31) == un
+    assert rotary(am, heads(am, its=1 << 38)) == un and rotary(am, heads(am, ots=1 << 40)) == un
     # the two outputs meet, or one output meets the other's input
     assert rotary(am, heads(am), heads(am, src=at(4), out=at(1))) == bad
     assert rotary(am, heads(am), heads(am, src=at(4), out=at(0))) == bad
