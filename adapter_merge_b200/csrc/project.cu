@@ -60,22 +60,24 @@ struct StreamArgs : ProjectArgs {
     uint32_t tmem_cols, stage_bytes;
 };
 
+__device__ __forceinline__ void add_bf16x4(float (&v)[4], uint2 w)
+{
+    v[0] += bf16lo(w.x); v[1] += bf16hi(w.x); v[2] += bf16lo(w.y); v[3] += bf16hi(w.y);
+}
+
 // bias, activation, product and residual of 4 consecutive outputs, and their store
 template <bool kGated>
-__device__ __forceinline__ void finish4(const StreamArgs& a, float (&v)[4], float (&u)[4], int64_t t, int o)
+__device__ __forceinline__ void finish4(const StreamArgs& a, float (&v)[4], float (&u)[4], uint2 bias, uint2 bias_up,
+                                        uint2 residual, int64_t t, int o)
 {
-    const auto add = [](float (&d)[4], const uint16_t* p) {
-        const uint2 w = *reinterpret_cast<const uint2*>(p);
-        d[0] += bf16lo(w.x); d[1] += bf16hi(w.x); d[2] += bf16lo(w.y); d[3] += bf16hi(w.y);
-    };
-    if (a.bias) add(v, a.bias + o);
+    if (a.bias) add_bf16x4(v, bias);
     activate_all(v, a.act);
     if constexpr (kGated) {
-        if (a.bias_up) add(u, a.bias_up + o);
+        if (a.bias_up) add_bf16x4(u, bias_up);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] *= u[i];
     } else {
-        if (a.residual) add(v, a.residual + t * a.ldr + o);
+        if (a.residual) add_bf16x4(v, residual);
     }
     if (!kGated && a.y_f32)
         *reinterpret_cast<float4*>(static_cast<float*>(a.y) + t * a.ldy + o) = make_float4(v[0], v[1], v[2], v[3]);
@@ -269,6 +271,24 @@ __global__ void __launch_bounds__(kStreamThreads, 2) stream_kernel(const __grid_
     const auto tokens_of = [&](int r) { return max(0, min(own, ntok - r * own)); };
     const int here = tokens_of(rank);
     bool ours = true;
+    // A warp takes a token's 128 outputs, four per lane, and every eighth of its
+    // CTA's tokens.  What the epilogue reads from memory is under way while the
+    // sums come together, then four tokens ahead.
+    constexpr int kWarps = kStreamThreads / 32, kAhead = 4;
+    const int o = row0 + lane * 4;
+    const auto read4 = [](const uint16_t* p, int64_t at) { return *reinterpret_cast<const uint2*>(p + at); };
+    uint2 bias = {}, bias_up = {}, residual[kAhead] = {};
+    const auto read_residuals = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (!kGated && a.residual && o < a.N && i + j * kWarps < here)
+                residual[j] = read4(a.residual, (t0 + rank * own + i + j * kWarps) * a.ldr + o);
+    };
+    if (o < a.N) {
+        if (a.bias) bias = read4(a.bias, o);
+        if (kGated && a.bias_up) bias_up = read4(a.bias_up, o);
+    }
+    read_residuals(warp);
     if (a.splits > 1) {
         if (threadIdx.x == 0 && here)
             mbar_arrive_expect_tx(&joined, (uint32_t)((a.splits - 1) * kParts * here * kTileM) * 4u);
@@ -287,19 +307,23 @@ __global__ void __launch_bounds__(kStreamThreads, 2) stream_kernel(const __grid_
         ours = !here || mbar_wait_hot(&joined, 0, &abort_flag);
         cluster_arrive();           // what came here has left the others
     }
-    // A warp takes a token's 128 outputs, four per lane.
     const bool fine = ours && !*(volatile int*)&abort_flag;
-    const int o = row0 + lane * 4;
     if (fine && o < a.N)
-        for (int i = warp; i < here; i += kStreamThreads / 32) {
-            float v[4], u[4];
-            const uint32_t at = (uint32_t)(i * kTileM + lane * 4) * 4u;
-            const uint32_t mine = sums + (uint32_t)(rank * own * kTileM) * 4u + at;
-            sum_ranks(v, mine, theirs + at, step, rank, a.splits);
-            if constexpr (kGated)
-                sum_ranks(u, mine + (uint32_t)(a.tile * kTileM) * 4u, theirs + (uint32_t)(own * kTileM) * 4u + at, step,
-                          rank, a.splits);
-            finish4<kGated>(a, v, u, t0 + rank * own + i, o);
+        for (int i0 = warp; i0 < here; i0 += kAhead * kWarps) {
+            if (i0 != warp) read_residuals(i0);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int i = i0 + j * kWarps;
+                if (i >= here) break;
+                float v[4], u[4];
+                const uint32_t at = (uint32_t)(i * kTileM + lane * 4) * 4u;
+                const uint32_t mine = sums + (uint32_t)(rank * own * kTileM) * 4u + at;
+                sum_ranks(v, mine, theirs + at, step, rank, a.splits);
+                if constexpr (kGated)
+                    sum_ranks(u, mine + (uint32_t)(a.tile * kTileM) * 4u,
+                              theirs + (uint32_t)(own * kTileM) * 4u + at, step, rank, a.splits);
+                finish4<kGated>(a, v, u, bias, bias_up, residual[j], t0 + rank * own + i, o);
+            }
         }
     if (threadIdx.x == 0 && !fine && a.status) atomicOr(a.status, ADAFUSE_STATUS_TIMEOUT);
     if (a.splits > 1) cluster_wait();       // the others' copies of this CTA's sums are done
@@ -363,18 +387,19 @@ StreamForm stream_form(const ProjectCall& c, int dev)
     const ProjectArgs& a = c.a;
     const double places = device_sms();
     constexpr int kMats = kGated ? 2 : 1;
-    int last = 0;
+    int64_t last = 0;
     for (int most = 128 / kMats; most <= 256 / kMats; most *= 2) {
         StreamForm f;
         f.n_tt = (int)((a.T + most - 1) / most);
         if (f.n_tt == last) break;
         last = f.n_tt;
         f.tile = (int)(((a.T + f.n_tt - 1) / f.n_tt + 15) / 16 * 16);       // of equal height
+        f.n_tt = (int)((a.T + f.tile - 1) / f.tile);
         const uint32_t stage = kMats * kWTile + (uint32_t)f.tile * kChunkK * 2;
         const int64_t blocks = (int64_t)((a.N + kTileM - 1) / kTileM) * f.n_tt;
         const double tall = f.tile * kMats;
         const double chunk = kGated ? std::max(500., 4 * tall) : std::max(365., 2.9 * tall);
-        const double memory = 2. * kMats * a.N * c.K / 3400;
+        const double memory = 2. * ((double)kMats * a.N * c.K + (double)a.T * (c.K + a.N)) / 3400;
         for (int two = 0; two < 2; ++two)
             for (int S = 1; S <= kMaxSplits && S <= a.chunks; ++S) {
                 // its own and the others' partial sums lie over the ring in the end
@@ -429,15 +454,12 @@ int launch_stream(ProjectCall& c, const StreamForm& f)
                               f.half ? kSmemHalf : kSmemFull, a.splits, c.s, xm, wm, um, a);
 }
 
-// Up to this many tokens W may stream past them; beyond, and where the estimate
-// is lower (4096 -> 4096 from 257 tokens on, 4096 -> 11008 from 129), tiles of
-// tokens and outputs on CTA pairs.
-constexpr int64_t kStreamTokens = 1024;
-
+// W streams past the tokens, or tiles of tokens and outputs on CTA pairs, by the
+// lower estimate (4096 -> 4096: tiles from 257 tokens on, 4096 -> 11008: from
+// 129; 6888 -> 144: from 4000 or so, as only the stream splits d_in).
 template <bool kGated>
 int launch_project(ProjectCall& c)
 {
-    if (c.a.T > kStreamTokens) return launch_project_tile(c);
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return ADAFUSE_ERR_DEVICE;
     const StreamForm f = stream_form<kGated>(c, dev);

@@ -149,6 +149,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     const int rank = (int)cluster_rank();
     const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
+    if (warp == 2 && elect_one()) {
+        prefetch_map(&xmap);
+        prefetch_map(kGated && rank ? &umap : &wmap);
+    }
     if (threadIdx.x == 0) {
         abort_flag = 0;
         for (int i = 0; i < kStages; ++i) {

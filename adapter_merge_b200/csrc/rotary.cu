@@ -15,8 +15,8 @@
 // lane then keeps those of its own elements), then its lanes rotate the heads:
 // an item is a vector of V elements together with the vector of its partners
 // (one vector that holds both in the interleaved layout, one unrotated vector
-// past `rot`), and 2^n lanes share a head, one item each, so that the norm's
-// sum is a shuffle among them.  A lane loads its next heads' items before it
+// past `rot`), and as many neighbouring lanes as a head has items share it, so
+// that the norm's sum is a shuffle among them.  A lane loads its next heads' items before it
 // rotates those it has.  No barrier across warps.
 #include <cuda_bf16.h>
 
@@ -49,7 +49,8 @@ struct RotArgs {
     int64_t T;
     int32_t Hq, H;          // query heads, all heads
     int32_t D, rot, half;
-    int32_t lanes;          // lanes per head: a power of two
+    int32_t lanes;          // lanes per head
+    int32_t first_step;     // half of the next power of two
     int32_t items;          // items per head
     int32_t warps, warps_log2;      // warps per token: a power of two
     int32_t pairs, pos32;
@@ -138,6 +139,17 @@ struct Item {
     }
 };
 
+// The sum over the lanes that share a head, in all of them: lane `sub` of a
+// group of any size adds up those behind it, the first one's sum goes to all.
+__device__ __forceinline__ float head_sum(const RotArgs& a, float v, int sub, int group)
+{
+    for (int d = a.first_step; d; d >>= 1) {
+        const float w = __shfl_down_sync(0xffffffffu, v, d);
+        if (sub + d < a.lanes) v += w;
+    }
+    return __shfl_sync(0xffffffffu, v, group * a.lanes & 31);
+}
+
 // The token's sines and cosines times the factor, by one warp.
 __device__ __forceinline__ void turn_token(const RotArgs& a, int64_t t, float* cosv, float* sinv)
 {
@@ -202,7 +214,7 @@ __device__ __forceinline__ void store_raw(const Raw<V>& r, uint16_t* p)
 // elements of one.
 template <int V, bool kPairs, bool kNorm>
 __device__ __forceinline__ void rotate_heads(const RotArgs& a, const Heads& m, int n, int64_t t, int h0, int stride,
-                                             int group, const Item<V>& it, bool mine, const float* cosv,
+                                             int group, int sub, const Item<V>& it, bool mine, const float* cosv,
                                              const float* sinv)
 {
     constexpr int H = V / 2;                        // words of a vector
@@ -282,8 +294,7 @@ __device__ __forceinline__ void rotate_heads(const RotArgs& a, const Heads& m, i
                     const float2 f = s.get();
                     sum = f.x + f.y;
                 }
-                for (int d = a.lanes / 2; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                const float f = rsqrtf(sum * a.inv_d + a.eps);
+                const float f = rsqrtf(head_sum(a, sum, sub, group) * a.inv_d + a.eps);
                 r = Two(f, f);
             }
             if (live) {
@@ -331,19 +342,19 @@ __global__ void __launch_bounds__(kRotThreads, 5) rotary_kernel(const RotArgs a)
     float* cosv = angles + warp * 2 * a.half;
     float* sinv = cosv + a.half;
     turn_token(a, t, cosv, sinv);
-    const int sub = lane & (a.lanes - 1), group = lane / a.lanes;
+    const int group = lane / a.lanes, sub = lane - group * a.lanes;
     const int per = 32 / a.lanes, stride = per * a.warps;
     const int first = ((int)w & (a.warps - 1)) * per + group;
     const Item<V> it(a, sub);
-    const bool mine = sub < a.items;
+    const bool mine = group < per;          // lanes past the last whole head idle
     if (kNorm && a.q.weight)
-        rotate_heads<V, kPairs, true>(a, a.q, a.Hq, t, first, stride, group, it, mine, cosv, sinv);
+        rotate_heads<V, kPairs, true>(a, a.q, a.Hq, t, first, stride, group, sub, it, mine, cosv, sinv);
     else
-        rotate_heads<V, kPairs, false>(a, a.q, a.Hq, t, first, stride, group, it, mine, cosv, sinv);
+        rotate_heads<V, kPairs, false>(a, a.q, a.Hq, t, first, stride, group, sub, it, mine, cosv, sinv);
     if (kNorm && a.k.weight)
-        rotate_heads<V, kPairs, true>(a, a.k, a.H - a.Hq, t, first, stride, group, it, mine, cosv, sinv);
+        rotate_heads<V, kPairs, true>(a, a.k, a.H - a.Hq, t, first, stride, group, sub, it, mine, cosv, sinv);
     else
-        rotate_heads<V, kPairs, false>(a, a.k, a.H - a.Hq, t, first, stride, group, it, mine, cosv, sinv);
+        rotate_heads<V, kPairs, false>(a, a.k, a.H - a.Hq, t, first, stride, group, sub, it, mine, cosv, sinv);
 }
 
 // Any head: a warp walks its items, twice for a norm.
@@ -359,10 +370,10 @@ __global__ void __launch_bounds__(kRotThreads) rotary_any_kernel(const RotArgs a
     float* cosv = angles + warp * 2 * a.half;
     float* sinv = cosv + a.half;
     turn_token(a, t, cosv, sinv);
-    const int sub = lane & (a.lanes - 1), group = lane / a.lanes;
+    const int group = lane / a.lanes, sub = lane - group * a.lanes;
     const int per = 32 / a.lanes;
     for (int h = ((int)w & (a.warps - 1)) * per + group; h - group < a.H; h += per * a.warps) {
-        const bool live = h < a.H;
+        const bool live = h < a.H && group < per;
         const Heads& m = h < a.Hq ? a.q : a.k;
         const int64_t hh = !live ? 0 : h < a.Hq ? h : h - a.Hq;
         const uint16_t* in = m.in + t * m.its + hh * m.ihs;
@@ -378,8 +389,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_any_kernel(const RotArgs a
                 sum += y.squares();
             }
         }
-        for (int d = a.lanes / 2; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        const float r = rsqrtf(sum * a.inv_d + a.eps);
+        const float r = rsqrtf(head_sum(a, sum, sub, group) * a.inv_d + a.eps);
         for (int j = sub; live && j < a.items; j += a.lanes) {
             const Item<V> it(a, j);
             x.load(in + it.o1);
@@ -533,8 +543,8 @@ extern "C" int adafuse_rotary(const adafuse_heads* q, const adafuse_heads* k, in
     int V = fits(8) && items(8) <= 32 ? 8 : fits(4) ? 4 : 1;
     a.items = items(V);
     const bool one = V > 1 && a.items <= 32;
-    a.lanes = 1;
-    while (a.lanes < 32 && a.lanes < a.items) a.lanes *= 2;
+    a.lanes = std::min(32, a.items);
+    while (2 * a.first_step < a.lanes) a.first_step = std::max(1, 2 * a.first_step);
     const int sms = device_sms();
     if (!sms) return ADAFUSE_ERR_DEVICE;
     // Warps per token: one while a lane has at most kLaneHeads heads (each
