@@ -31,8 +31,8 @@ constexpr int kEpiWarps = 8;
 constexpr int kPairTokens = 256;
 constexpr int kGroup = 8;                       // token tiles per group of the walk
 constexpr uint32_t kTileSmem = 226 * 1024;      // the whole SM: no other tcgen05 kernel beside a pair
-constexpr uint32_t kRowPitch = 80;              // 64 bytes of a row and 16 of padding
-constexpr uint32_t kTurnBytes = kEpiWarps * 32 * kRowPitch;
+constexpr uint32_t kBox = 32 * 128;             // a warp's box of outputs: 32 rows of up to 128 bytes
+constexpr uint32_t kTurnBytes = kEpiWarps * kBox;
 constexpr uint32_t kXBytes = 128 * kChunkK * 2; // a CTA's tokens of a chunk
 
 // A stage holds one chunk of a wide tile, two of a narrow one: the waits and
@@ -50,7 +50,7 @@ struct Ring {
 struct TileArgs : ProjectArgs {
     int32_t m_tiles, n_tiles, out_cols;         // outputs per tile
     int32_t part;                               // chunks per accumulator
-    int64_t tiles;
+    uint32_t tiles;
 };
 
 // Adds p[0 .. N) (bf16, 16-byte aligned) to v; groups of 8 from `limit` on are not read.
@@ -78,56 +78,83 @@ __device__ __forceinline__ void load_cols(uint32_t taddr, float (&v)[N])
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// A warp's 32 rows x 64 bytes, one row per lane as `w`, written to y with four
-// lanes per row.  `limit`: bytes of a row that y has.
-__device__ __forceinline__ void store_rows(uint8_t* turn, const uint4 (&w)[4], uint8_t* y, int64_t pitch, int64_t rows,
-                                           int limit)
-{
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(turn + lane * kRowPitch + i * 16) = w[i];
-    __syncwarp();
-    const int piece = (lane & 3) * 16;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + (lane >> 2);
-        const uint4 v = *reinterpret_cast<const uint4*>(turn + r * kRowPitch + piece);
-        if (r < rows && piece < limit) *reinterpret_cast<uint4*>(y + r * pitch + piece) = v;
-    }
-    __syncwarp();
-}
-
 __device__ __forceinline__ uint4 pack8(const float* v)
 {
     return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                       pack_bf16x2(v[6], v[7]));
 }
 
-// 32 finished columns (outputs o ..) of the warp's 32 tokens (t0 ..): bias and
-// activation are done by the caller where a factor follows them.
-template <bool kF32>
-__device__ __forceinline__ void finish32(const TileArgs& a, float (&v)[32], int64_t t0, int o, uint8_t* turn)
-{
-    const int lane = threadIdx.x & 31;
-    const int cols = a.N - o;           // outputs that exist from o on
-    const int64_t rows = a.T - t0;
-    if (a.residual && lane < rows) add_bf16(v, a.residual + (t0 + lane) * a.ldr + o, cols);
-    if constexpr (kF32) {
-        float* y = static_cast<float*>(a.y) + t0 * a.ldy + o;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint4 w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = make_uint4(__float_as_uint(v[16 * h + 4 * i]), __float_as_uint(v[16 * h + 4 * i + 1]),
-                                  __float_as_uint(v[16 * h + 4 * i + 2]), __float_as_uint(v[16 * h + 4 * i + 3]));
-            store_rows(turn, w, reinterpret_cast<uint8_t*>(y + 16 * h), a.ldy * 4, rows, (cols - 16 * h) * 4);
-        }
-    } else {
-        uint16_t* y = static_cast<uint16_t*>(a.y) + t0 * a.ldy + o;
-        const uint4 w[4] = {pack8(v), pack8(v + 8), pack8(v + 16), pack8(v + 24)};
-        store_rows(turn, w, reinterpret_cast<uint8_t*>(y), a.ldy * 2, rows, cols * 2);
+// Where a warp puts its outputs on their way to y: a box of 32 tokens x kRow
+// bytes in shared memory, in the layout that the tensor map of y swizzles, so
+// that lanes that write a row each meet no bank twice.
+template <int kRow>
+struct Box {
+    static_assert(kRow == 128 || kRow == 64, "a swizzled row");
+    uint8_t* at;
+    // 16 bytes of the lane's row
+    __device__ __forceinline__ void put(int piece, uint4 w) const
+    {
+        const int r = threadIdx.x & 31, turned = kRow == 128 ? piece ^ (r & 7) : piece ^ ((r >> 1) & 3);
+        *reinterpret_cast<uint4*>(at + r * kRow + turned * 16) = w;
     }
+    // the box may be written again once the copy of its last contents has read it
+    __device__ __forceinline__ void wait() const
+    {
+        bulk_wait_group_read<0>();
+        __syncwarp();
+    }
+    __device__ __forceinline__ void send(const CUtensorMap* y, int o, int t) const
+    {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (elect_one()) tma_store_2d(y, at, o, t);
+        bulk_commit_group();
+    }
+};
+
+// 32 residuals of a lane's token, outputs o .., loaded ahead of their use.
+struct Residual {
+    uint4 w[4];
+    __device__ __forceinline__ void load(const ProjectArgs& a, int64_t t, int o)
+    {
+        if (!a.residual || t >= a.T) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (o + 8 * i < a.N) w[i] = *reinterpret_cast<const uint4*>(a.residual + t * a.ldr + o + 8 * i);
+    }
+    __device__ __forceinline__ void add(const ProjectArgs& a, float (&v)[32]) const
+    {
+        if (!a.residual) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[8 * i] += bf16lo(w[i].x); v[8 * i + 1] += bf16hi(w[i].x);
+            v[8 * i + 2] += bf16lo(w[i].y); v[8 * i + 3] += bf16hi(w[i].y);
+            v[8 * i + 4] += bf16lo(w[i].z); v[8 * i + 5] += bf16hi(w[i].z);
+            v[8 * i + 6] += bf16lo(w[i].w); v[8 * i + 7] += bf16hi(w[i].w);
+        }
+    }
+};
+
+// Puts 32 finished columns of the lane's token into the box.
+template <bool kF32, int kRow>
+__device__ __forceinline__ void put32(const float (&v)[32], Box<kRow> box, int piece)
+{
+    if constexpr (kF32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            box.put(piece + i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                          __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) box.put(piece + i, pack8(v + 8 * i));
+    }
+}
+
+// Bytes of a row of a box.
+template <int kCols, bool kGated, bool kF32>
+__host__ __device__ constexpr int box_row()
+{
+    return kGated && kCols == 128 ? 64 : 128;
 }
 
 // kCols: accumulator columns of a tile.  kF32: fp32 outputs (never gated).
@@ -135,6 +162,7 @@ template <int kCols, bool kGated, bool kF32>
 __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_constant__ CUtensorMap xmap,
                                                                const __grid_constant__ CUtensorMap wmap,
                                                                const __grid_constant__ CUtensorMap umap,
+                                                               const __grid_constant__ CUtensorMap ymap,
                                                                const TileArgs a)
 {
     using R = Ring<kCols>;
@@ -147,7 +175,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     uint8_t* turns = ring + (size_t)kStages * R::kStage;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
-    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const uint32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (warp == 2 && elect_one()) {
         prefetch_map(&xmap);
@@ -178,14 +206,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
 
-    // tile i of the walk: groups of kGroup token tiles, token tiles fastest
-    const auto tile_at = [&](int64_t i, int& m, int& n) {
-        const int64_t per = (int64_t)kGroup * a.n_tiles;
-        const int64_t g = i / per;
-        const int rows = min(kGroup, a.m_tiles - (int)g * kGroup);
-        const int64_t j = i - g * per;
-        m = (int)g * kGroup + (int)(j % rows);
+    // tile i of the walk: groups of kGroup token tiles, token tiles fastest (in
+    // 32 bits: three 64-bit divisions by variables took 3000 cycles of every tile)
+    const auto tile_at = [&](uint32_t i, int& m, int& n) {
+        const uint32_t per = (uint32_t)(kGroup * a.n_tiles);
+        const uint32_t g = i / per;
+        const uint32_t rows = (uint32_t)min(kGroup, a.m_tiles - (int)g * kGroup);
+        const uint32_t j = i - g * per;
         n = (int)(j / rows);
+        m = (int)(g * kGroup + (j - (uint32_t)n * rows));
     };
 
     if (warp == 0) {
@@ -197,7 +226,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         int s = 0;                  // the ring's next stage
         uint32_t lap = 1;           // parity that its `empty` completes with when free (the first lap: at once)
         bool stop = false;
-        for (int64_t i = pair; i < a.tiles && !stop; i += pairs) {
+        for (uint32_t i = pair; i < a.tiles && !stop; i += pairs) {
             int m, n;
             tile_at(i, m, n);
             const int t = m * kPairTokens + rank * 128;
@@ -241,7 +270,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             const uint64_t xdesc = make_sdesc(smem_u32(ring), 16u, 1024u, kLayoutSw128);
             const uint64_t wdesc = make_sdesc(smem_u32(ring) + kXBytes, 16u, 1024u, kLayoutSw128);
             bool stop = false;
-            for (int64_t i = pair; i < a.tiles && !stop; i += pairs) {
+            for (uint32_t i = pair; i < a.tiles && !stop; i += pairs) {
                 int left = 0;           // stages until the next accumulator
                 for (int c = 0; c < a.chunks; c += R::kPer) {
                     const bool fresh = left == 0;
@@ -284,7 +313,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         __syncwarp();
     } else {
         const int q = warp & 3, half = (warp - 2) >> 2;
-        uint8_t* turn = turns + (warp - 2) * 32 * kRowPitch;
+        using B = Box<box_row<kCols, kGated, kF32>()>;
+        const B box{turns + (warp - 2) * kBox};
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
         const uint32_t free0 = cluster_map(smem_u32(&accempty[0]), 0), free1 = cluster_map(smem_u32(&accempty[1]), 0);
         uint32_t use = 0;
@@ -301,7 +331,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             if (lane == 0) mbar_arrive_cluster(use & 1 ? free1 : free0);
             ++use;
         };
-        for (int64_t i = pair; i < a.tiles; i += pairs) {
+        for (uint32_t i = pair; i < a.tiles; i += pairs) {
             int m, n;
             tile_at(i, m, n);
             const int64_t t0 = (int64_t)m * kPairTokens + rank * 128 + q * 32;
@@ -310,6 +340,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                 const int o0 = n * a.out_cols + half * kMine;
                 if (!take()) break;
                 const uint32_t d = lanes + (uint32_t)(use & 1) * kCols + half * kMine;
+                box.wait();
 #pragma unroll
                 for (int c = 0; c < kMine; c += 32) {
                     float v[32], u[32];
@@ -320,21 +351,29 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                     activate_all(v, a.act);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] *= u[j];
-                    finish32<false>(a, v, t0, o0 + c, turn);
+                    put32<false>(v, box, c / 8);
                 }
+                if (o0 < a.N && t0 < a.T) box.send(&ymap, o0, (int)t0);
                 give();
             } else if constexpr (!kF32) {
                 constexpr int kMine = kCols / 2;
                 const int o0 = n * a.out_cols + half * kMine;
+                Residual ahead[2];          // of the next two steps
+                ahead[0].load(a, t0 + lane, o0);
+                ahead[1].load(a, t0 + lane, o0 + 32);
                 if (!take()) break;
                 const uint32_t d = lanes + (uint32_t)(use & 1) * kCols + half * kMine;
-#pragma unroll 1
+#pragma unroll
                 for (int c = 0; c < kMine; c += 32) {
                     float v[32];
                     load_cols(d + c, v);
                     if (a.bias) add_bf16(v, a.bias + o0 + c, a.N - o0 - c);
                     activate_all(v, a.act);
-                    finish32<false>(a, v, t0, o0 + c, turn);
+                    ahead[c / 32 & 1].add(a, v);
+                    if (c + 64 < kMine) ahead[c / 32 & 1].load(a, t0 + lane, o0 + c + 64);
+                    if (!(c & 32)) box.wait();
+                    put32<false>(v, box, (c & 32) / 8);
+                    if ((c & 32) && o0 + c - 32 < a.N && t0 < a.T) box.send(&ymap, o0 + c - 32, (int)t0);
                 }
                 give();
             } else {
@@ -357,13 +396,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
 #pragma unroll
                 for (int c = 0; c < kParts; ++c) {
                     const int o = o0 + c * 32;
+                    Residual now;
+                    now.load(a, t0 + lane, o);
                     if (a.bias) add_bf16(v[c], a.bias + o, a.N - o);
                     activate_all(v[c], a.act);
-                    finish32<true>(a, v[c], t0, o, turn);
+                    now.add(a, v[c]);
+                    box.wait();
+                    put32<true>(v[c], box, 0);
+                    if (o < a.N && t0 < a.T) box.send(&ymap, o, (int)t0);
                 }
             }
         }
     }
+    if (warp >= 2) bulk_wait_group<0>();
     __syncthreads();
     if (threadIdx.x == 0 && *(volatile int*)&abort_flag && a.status) atomicOr(a.status, ADAFUSE_STATUS_TIMEOUT);
     cluster_sync();
@@ -373,6 +418,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     }
 }
 
+// Tensor map of y: boxes of 32 tokens x `row` bytes, swizzled by the row's length.
+bool encode_outputs(CUtensorMap* m, const ProjectArgs& a, int row)
+{
+    const cuuint64_t size = a.y_f32 ? 4 : 2;
+    cuuint64_t dims[2] = {(cuuint64_t)a.N, (cuuint64_t)a.T};
+    cuuint64_t strides[1] = {(cuuint64_t)(a.T > 1 ? a.ldy : (a.N + 7) / 8 * 8) * size};
+    cuuint32_t box[2] = {(cuuint32_t)(row / size), 32};
+    cuuint32_t estr[2] = {1, 1};
+    return tensor_map_encoder()(m, a.y_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.y,
+                                dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int kCols, bool kGated, bool kF32>
 int launch_tiles(ProjectCall& c, int pairs)
 {
@@ -380,7 +439,9 @@ int launch_tiles(ProjectCall& c, int pairs)
     a.out_cols = kGated ? kCols / 2 : kCols;
     a.m_tiles = (int)((a.T + kPairTokens - 1) / kPairTokens);
     a.n_tiles = (a.N + a.out_cols - 1) / a.out_cols;
-    a.tiles = (int64_t)a.m_tiles * a.n_tiles;
+    const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
+    if (tiles > 0x7fffffff || a.n_tiles > 0x7fffffff / kGroup) return ADAFUSE_ERR_UNSUPPORTED;
+    a.tiles = (uint32_t)tiles;
     a.part = kPartCols / kChunkK;
     auto kernel = tile_kernel<kCols, kGated, kF32>;
     static std::atomic<uint64_t> ready{0};          // devices whose kernel may use all shared memory
@@ -391,13 +452,14 @@ int launch_tiles(ProjectCall& c, int pairs)
             return ADAFUSE_ERR_CUDA;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    CUtensorMap xm, wm, um;
+    CUtensorMap xm, wm, um, ym;
     if (!encode_rows(&xm, c.x, a.T, c.K, c.ldx, 128) || !encode_rows(&wm, c.W, a.N, c.K, c.ldw, kCols / 2))
         return ADAFUSE_ERR_UNSUPPORTED;
     if (!kGated) um = wm;
     else if (!encode_rows(&um, c.W_up, a.N, c.K, c.ldw, kCols / 2)) return ADAFUSE_ERR_UNSUPPORTED;
-    const int64_t n = std::min<int64_t>(a.tiles, pairs);
-    return launch_pdl_cluster(kernel, dim3((unsigned)(2 * n)), dim3(kTileThreads), kTileSmem, 2, c.s, xm, wm, um, a);
+    if (!encode_outputs(&ym, a, box_row<kCols, kGated, kF32>())) return ADAFUSE_ERR_UNSUPPORTED;
+    const int64_t n = std::min<int64_t>(tiles, pairs);
+    return launch_pdl_cluster(kernel, dim3((unsigned)(2 * n)), dim3(kTileThreads), kTileSmem, 2, c.s, xm, wm, um, ym, a);
 }
 
 }  // namespace

@@ -404,25 +404,26 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
-// Every thread of every CTA of the cluster arrives and waits; what each wrote
-// to shared memory before is visible to the others after.
-__device__ __forceinline__ void cluster_sync()
-{
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
+// Every thread of every CTA of the cluster arrives, and waits for the others.
+// Relaxed: it orders no memory (a release would first wait for all accesses of
+// the thread, about 1000 cycles); what crosses CTAs here is ordered by
+// mbarriers and the fence after their initialisation.
 __device__ __forceinline__ void cluster_arrive()
 {
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void cluster_wait()
 {
     __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    cluster_arrive();
+    cluster_wait();
 }
 
 // Address of the cluster's CTA `rank` that corresponds to this CTA's own
@@ -493,9 +494,12 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar)
 }
 
 // Arrive on a barrier of another CTA of the cluster (a shared::cluster address).
+// It releases within the CTA only: at cluster scope it would wait for the
+// thread's outstanding accesses to memory, which took the epilogue of a
+// projection's tile 3000 cycles.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // ------------------------------------------------------------------ misc
