@@ -4,18 +4,24 @@
 // for x [T, d_in] and weights [d_out, d_in], everything in fp32 up to the one
 // rounding of y.
 //
-// stream_kernel: W streams once per tile of tokens, T up to a few hundred.
-// A unit is 128 rows of W (and the same 128 of W_up) against a tile of up to
-// 256 (128) tokens, with the W rows as the M side of the tensor-core product
-// and the tokens, padded to 16, as its N side, so that a single token costs
-// one pass over W.  A unit's d_in is split over the CTAs of a cluster: one
-// warp loads the CTA's range of 64-column chunks through a ring of shared
-// memory by TMA, two issue tcgen05.mma into TMEM, then the partial sums go
-// to shared memory (token by token), and each CTA adds up its share of the
-// tokens over the cluster's partials, always in rank order, applies the
-// epilogue and writes y.  No workspace, no counters, no atomics.  TMEM is
-// freed before a CTA waits for its cluster, so no CTA ever waits for another
-// while it holds TMEM that the other needs.
+// stream_kernel (decode batches, and long prompts of few outputs; otherwise the
+// tiles of project_tile.cu): W streams past a tile of tokens.  A unit is 128
+// rows of W (and the same 128 of W_up) against a tile of up to 256 (128)
+// tokens, with the W rows as the M side of the tensor-core product and the
+// tokens, padded to 16, as its N side, so that a single token costs one pass
+// over W.  A unit's d_in is split over the CTAs of a cluster: one warp loads
+// the CTA's range of 64-column chunks through a ring of shared memory by TMA,
+// two issue tcgen05.mma into TMEM, then the partial sums go to shared memory
+// (token by token), each CTA gets the others' sums of its share of the tokens
+// by bulk copies, adds them in rank order, applies the epilogue and writes y.
+// No workspace, no counters, no atomics.  TMEM is freed before a CTA waits for
+// its cluster, so no CTA ever waits for another while it holds TMEM that the
+// other needs.
+//
+// Bound by W's bytes: one token through 4096 -> 11008 gate and up (180 MB) 31.6
+// us, 5.7 TB/s; 64 tokens through 5120 -> 13824 (283 MB) 50.4 us, 5.6 TB/s.  A
+// single 4096 x 4096 layer (33.5 MB, 5.1 us) takes 8.6: the launch, the first
+// load's way (1.2 us) and the sum over the cluster (1 us) are not hidden.
 //
 // The tensor core rounds each step of an accumulator towards zero, which adds
 // up over long sums (measured against 64 bits: 4.4e-6 relative at d_in = 4096,
@@ -48,7 +54,7 @@ bool encode_rows(CUtensorMap* m, const void* p, int64_t rows, int32_t cols, int6
 
 namespace {
 
-constexpr int kStreamThreads = 256;                     // one warp loads, one multiplies; all finish
+constexpr int kStreamThreads = 256;                     // one warp loads, two multiply; all finish
 constexpr int kMaxRing = 12;                            // stages of at least 18 KB
 constexpr int kMaxSplits = 8;
 constexpr uint32_t kWTile = kTileM * kChunkK * 2;       // 16 KB
@@ -366,11 +372,13 @@ int clusters_at_once(int dev, int splits)
 // How a call runs on the stream kernel.
 struct StreamForm {
     int tile = 0, n_tt = 0, splits = 0, ring = 0;
+    int parts = 1;              // accumulators of each multiplying warp (plain)
     bool half = false;
     double cost = 0;            // estimated cycles
 };
 
-// The cheapest form: tiles of up to 128 tokens (gated 64) or twice that; one
+// The cheapest form, if there is one: tiles of up to 128 tokens (gated 64) or
+// twice that (fp32: from 32 on, as more parts need more accumulators); one
 // CTA per SM with a deep ring, or two (where a ring and the partial sums fit
 // half of shared memory); and the split of d_in.  Measured: a chunk takes a CTA
 // 365 cycles (gated 500), more for tall tiles; memory gives W's bytes at 3400 a
@@ -388,10 +396,10 @@ StreamForm stream_form(const ProjectCall& c, int dev)
     const double places = device_sms();
     constexpr int kMats = kGated ? 2 : 1;
     int64_t last = 0;
-    for (int most = 128 / kMats; most <= 256 / kMats; most *= 2) {
+    for (int most = a.y_f32 ? 32 : 128 / kMats; most <= 256 / kMats; most *= 2) {
         StreamForm f;
         f.n_tt = (int)((a.T + most - 1) / most);
-        if (f.n_tt == last) break;
+        if (f.n_tt == last) continue;
         last = f.n_tt;
         f.tile = (int)(((a.T + f.n_tt - 1) / f.n_tt + 15) / 16 * 16);       // of equal height
         f.n_tt = (int)((a.T + f.tile - 1) / f.tile);
@@ -408,8 +416,13 @@ StreamForm stream_form(const ProjectCall& c, int dev)
                 f.ring = (int)std::min<uint32_t>(kMaxRing, room / stage);
                 if (!kGated) f.ring &= ~1;              // even, see the multiplying warps
                 if (sums > room || f.ring < (kGated ? 3 : 4)) continue;
+                if (a.y_f32) {                          // as many accumulators as its parts need
+                    f.parts = ((a.chunks + S - 1) / S + 1) / 2;
+                    f.parts = (f.parts * kChunkK + kPartCols - 1) / kPartCols;
+                    if (f.parts * 2 * f.tile > (two ? 256 : 512)) continue;
+                }
                 const int at_once = clusters_at_once<kGated>(dev, S) * (1 + two);
-                if (!at_once) continue;
+                if (!at_once || blocks * S > 0x7fffffff) continue;
                 const int64_t rounds = (blocks + at_once - 1) / at_once;
                 const double taken = (double)blocks * S / (rounds * places * (1 + two));
                 const double work = (double)rounds * ((a.chunks + S - 1) / S) * chunk * (two ? 1.6 : 1.);
@@ -434,16 +447,9 @@ int launch_stream(ProjectCall& c, const StreamForm& f)
     a.ring = f.ring;
     a.stage_bytes = (kGated ? 2 : 1) * kWTile + (uint32_t)a.tile * kChunkK * 2;
     const int64_t blocks = (int64_t)((a.N + kTileM - 1) / kTileM) * a.n_tt;
-    // accumulators of a plain unit: `parts` for each of the two multiplying warps
-    a.parts = 1;
-    if (a.y_f32) {
-        const int per = (a.chunks + a.splits - 1) / a.splits;
-        a.parts = std::min((f.half ? 256 : 512) / (2 * a.tile), (per * kChunkK / 2 + kPartCols - 1) / kPartCols);
-        a.parts = std::max(1, std::min(a.parts, a.chunks / a.splits / 2));
-    }
+    a.parts = std::max(1, std::min(f.parts, a.chunks / a.splits / 2));         // a part has a chunk at least
     a.tmem_cols = 32;
     while ((int)a.tmem_cols < a.tile * a.parts * 2) a.tmem_cols *= 2;
-    if (blocks * a.splits > 0x7fffffff) return ADAFUSE_ERR_UNSUPPORTED;
 
     CUtensorMap xm, wm, um;
     if (!encode_rows(&xm, c.x, a.T, c.K, c.ldx, a.tile) || !encode_rows(&wm, c.W, a.N, c.K, c.ldw, kTileM))

@@ -6,12 +6,18 @@
 // other the up rows of the same outputs, so the two halves of a tile's columns
 // are act's argument and its factor), and holds the accumulator of its own 128
 // tokens in TMEM, twice, so the epilogue of one tile runs under the products
-// of the next.  One warp per CTA loads by TMA into a ring, one thread of the
-// pair issues the products, eight warps of each CTA read the accumulator, add
-// the bias, the activation, the factor and the residual in fp32, round, and
-// turn the rows through shared memory so that every store writes whole
-// sectors.  The pairs are persistent and walk the tiles in groups of eight
-// token tiles, so that the tiles in flight share both operands in L2.
+// of the next.  One warp per CTA loads by TMA into a ring, one warp of the pair
+// issues the products, eight warps of each CTA read the accumulator, add the
+// bias, the activation, the factor and the residual in fp32, round, and send
+// boxes of 32 tokens to y by TMA.  The pairs are persistent and walk the tiles
+// in groups of eight token tiles, so that the tiles in flight share both
+// operands in L2.
+//
+// A 64-column chunk of a wide tile takes 505 cycles, the products' own time;
+// beyond a few milliseconds of work the board's power limit sets the clock
+// (1.2-1.5 GHz of 1.97), which is then what bounds the call: 4096 tokens, 11008
+// -> 4096, 300 us (1.23 PFLOP/s; the library's plain product 279 us on such a
+// board), 2001 tokens through the 7B gate and up, 277 us (1.30 PFLOP/s).
 //
 // fp32 outputs take a fresh accumulator every 512 columns of d_in, added up in
 // the epilogue's registers (the tensor core's rounding towards zero adds up
@@ -112,6 +118,17 @@ struct Box {
     }
 };
 
+__device__ __forceinline__ void add_bf16(float (&v)[32], const uint4 (&w)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[8 * i] += bf16lo(w[i].x); v[8 * i + 1] += bf16hi(w[i].x);
+        v[8 * i + 2] += bf16lo(w[i].y); v[8 * i + 3] += bf16hi(w[i].y);
+        v[8 * i + 4] += bf16lo(w[i].z); v[8 * i + 5] += bf16hi(w[i].z);
+        v[8 * i + 6] += bf16lo(w[i].w); v[8 * i + 7] += bf16hi(w[i].w);
+    }
+}
+
 // 32 residuals of a lane's token, outputs o .., loaded ahead of their use.
 struct Residual {
     uint4 w[4];
@@ -124,14 +141,7 @@ struct Residual {
     }
     __device__ __forceinline__ void add(const ProjectArgs& a, float (&v)[32]) const
     {
-        if (!a.residual) return;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[8 * i] += bf16lo(w[i].x); v[8 * i + 1] += bf16hi(w[i].x);
-            v[8 * i + 2] += bf16lo(w[i].y); v[8 * i + 3] += bf16hi(w[i].y);
-            v[8 * i + 4] += bf16lo(w[i].z); v[8 * i + 5] += bf16hi(w[i].z);
-            v[8 * i + 6] += bf16lo(w[i].w); v[8 * i + 7] += bf16hi(w[i].w);
-        }
+        if (a.residual) add_bf16(v, w);
     }
 };
 
@@ -358,19 +368,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             } else if constexpr (!kF32) {
                 constexpr int kMine = kCols / 2;
                 const int o0 = n * a.out_cols + half * kMine;
-                Residual ahead[2];          // of the next two steps
-                ahead[0].load(a, t0 + lane, o0);
-                ahead[1].load(a, t0 + lane, o0 + 32);
+                Residual ahead;             // of the next step
+                ahead.load(a, t0 + lane, o0);
+                uint4 bias[4];
+                const auto load_bias = [&](int o) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (a.bias && o + 8 * i < a.N) bias[i] = *reinterpret_cast<const uint4*>(a.bias + o + 8 * i);
+                };
+                load_bias(o0);
                 if (!take()) break;
                 const uint32_t d = lanes + (uint32_t)(use & 1) * kCols + half * kMine;
 #pragma unroll
                 for (int c = 0; c < kMine; c += 32) {
                     float v[32];
                     load_cols(d + c, v);
-                    if (a.bias) add_bf16(v, a.bias + o0 + c, a.N - o0 - c);
+                    if (a.bias) add_bf16(v, bias);
+                    if (c + 32 < kMine) load_bias(o0 + c + 32);
                     activate_all(v, a.act);
-                    ahead[c / 32 & 1].add(a, v);
-                    if (c + 64 < kMine) ahead[c / 32 & 1].load(a, t0 + lane, o0 + c + 64);
+                    ahead.add(a, v);
+                    if (c + 32 < kMine) ahead.load(a, t0 + lane, o0 + c + 32);
                     if (!(c & 32)) box.wait();
                     put32<false>(v, box, (c & 32) / 8);
                     if ((c & 32) && o0 + c - 32 < a.N && t0 < a.T) box.send(&ymap, o0 + c - 32, (int)t0);

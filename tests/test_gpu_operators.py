@@ -253,8 +253,8 @@ def test_projections_are_deterministic(am, T):
 def test_fp32_sums_stay_near_fp32_over_long_rows(am):
     """Parts of at most 512 columns: an error that grows with d_in would be
     1.2e-5 relative at 11008 columns (measured for one accumulator)."""
-    for T in (4, 200, 600):
-        x, W = rnd(T, 11008), rnd(256, 11008, seed=1, std=0.02)
+    for T, N in ((4, 256), (200, 256), (600, 256), (16, 13824), (100, 13824), (256, 5120), (1500, 1024)):
+        x, W = rnd(T, 11008), rnd(N, 11008, seed=1, std=0.02)
         want = x.to(F64) @ W.to(F64).t()
         y = am.project(x, W, out_dtype=F32).to(F64)
         assert float((y - want).norm() / want.norm()) < 1.5e-6
