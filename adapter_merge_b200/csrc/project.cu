@@ -310,7 +310,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2) stream_kernel(const __grid_
                                       (uint32_t)(count * kTileM) * 4u, cluster_map(smem_u32(&joined), (uint32_t)r));
             }
         __syncwarp();
-        ours = !here || mbar_wait_hot(&joined, 0, &abort_flag);
+        // also after an abort: the copies have to land before the CTA may leave
+        ours = !here || mbar_wait_hot(&joined, 0, &abort_flag) || mbar_wait_landed(&joined, 0);
         cluster_arrive();           // what came here has left the others
     }
     const bool fine = ours && !*(volatile int*)&abort_flag;
@@ -461,8 +462,9 @@ int launch_stream(ProjectCall& c, const StreamForm& f)
 }
 
 // W streams past the tokens, or tiles of tokens and outputs on CTA pairs, by the
-// lower estimate (4096 -> 4096: tiles from 257 tokens on, 4096 -> 11008: from
-// 129; 6888 -> 144: from 4000 or so, as only the stream splits d_in).
+// lower estimate (256 tokens, 4096 -> 4096: 16.2 us streamed, 17.8 in tiles;
+// 384: 21.5 and 18.0; 256, 4096 -> 11008: 40.7 and 28.3; 2869, 6888 -> 144: 29
+// and 37, as only the stream splits d_in).
 template <bool kGated>
 int launch_project(ProjectCall& c)
 {
@@ -479,7 +481,8 @@ int check(ProjectCall& c, const void* bias, const void* bias_up, bool gated, uin
     const uint32_t act = flags & ADAFUSE_ACT_MASK;
     if (flags & ~(ADAFUSE_ACT_MASK | ADAFUSE_TEST_STALL | (gated ? 0u : ADAFUSE_OUT_F32))) return ADAFUSE_ERR_INVALID_ARG;
     if (a.T < 0 || c.K < 1 || a.N < 1) return ADAFUSE_ERR_INVALID_ARG;
-    if (act > ADAFUSE_ACT_GELU_TANH || c.K % 8 || a.N % 8 || a.T > 0x7fffff00) return ADAFUSE_ERR_UNSUPPORTED;
+    if (act > ADAFUSE_ACT_GELU_TANH || c.K % 8 || a.N % 8 || a.T > 0x7fffff00 || a.N > 0x7fffff00 ||
+        c.K > 0x7fffff00) return ADAFUSE_ERR_UNSUPPORTED;
     if (a.T == 0) return ADAFUSE_OK;
     if (!c.x || !c.W || !a.y || (gated && !c.W_up)) return ADAFUSE_ERR_INVALID_ARG;
     a.y_f32 = flags & ADAFUSE_OUT_F32 ? 1 : 0;

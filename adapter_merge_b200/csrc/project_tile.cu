@@ -38,7 +38,7 @@ constexpr int kPairTokens = 256;
 constexpr int kGroup = 8;                       // token tiles per group of the walk
 constexpr uint32_t kTileSmem = 226 * 1024;      // the whole SM: no other tcgen05 kernel beside a pair
 constexpr uint32_t kBox = 32 * 128;             // a warp's box of outputs: 32 rows of up to 128 bytes
-constexpr uint32_t kTurnBytes = kEpiWarps * kBox;
+constexpr uint32_t kBoxBytes = kEpiWarps * kBox;
 constexpr uint32_t kXBytes = 128 * kChunkK * 2; // a CTA's tokens of a chunk
 
 // A stage holds one chunk of a wide tile, two of a narrow one: the waits and
@@ -50,7 +50,7 @@ struct Ring {
     static constexpr uint32_t kWBytes = kCols / 2 * kChunkK * 2;
     static constexpr uint32_t kChunk = kXBytes + kWBytes;
     static constexpr uint32_t kStage = kPer * kChunk;
-    static constexpr int kStages = (int)((kTileSmem - 1024 - kTurnBytes) / kStage);
+    static constexpr int kStages = (int)((kTileSmem - 1024 - kBoxBytes) / kStage);
 };
 
 struct TileArgs : ProjectArgs {
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
-    uint8_t* turns = ring + (size_t)kStages * R::kStage;
+    uint8_t* boxes = ring + (size_t)kStages * R::kStage;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
     const uint32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     } else {
         const int q = warp & 3, half = (warp - 2) >> 2;
         using B = Box<box_row<kCols, kGated, kF32>()>;
-        const B box{turns + (warp - 2) * kBox};
+        const B box{boxes + (warp - 2) * kBox};
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
         const uint32_t free0 = cluster_map(smem_u32(&accempty[0]), 0), free1 = cluster_map(smem_u32(&accempty[1]), 0);
         uint32_t use = 0;

@@ -435,19 +435,30 @@ bool vectors_fit(const adafuse_heads* m, int V, int T)
     return aligned_to(m->in, 2 * V) && aligned_to(m->out, 2 * V) && aligned_to(m->weight, 2 * V);
 }
 
-int64_t span(int64_t T, int64_t ts, int32_t heads, int64_t hs, int32_t D)
-{
-    return (T - 1) * ts + (int64_t)(heads - 1) * hs + D;
-}
+// Elements from a token's first head to the end of its last.
+int64_t token_span(int32_t heads, int64_t head_stride, int32_t D) { return (int64_t)(heads - 1) * head_stride + D; }
+
+// Heads as the overlap checks see them.
+struct Span {
+    const void* base;
+    int64_t token_stride, head_stride;
+    int32_t heads;
+};
 
 // Whether two sets of heads can share an element.  Sets whose address ranges
 // cross are told apart where they have the same token stride and each token's
-// heads lie within it (columns of one buffer).
-bool heads_overlap(const void* p, int64_t pts, int64_t phs, int32_t ph, const void* q, int64_t qts, int64_t qhs,
-                   int32_t qh, int64_t T, int32_t D)
+// heads lie within it (columns of one buffer), or the same head stride, of
+// which the token stride is a multiple (q, k and v of a head side by side).
+bool heads_overlap(const Span& p, const Span& q, int64_t T, int32_t D)
 {
-    return rows_overlap(RowSpan{p, T, 2 * span(1, 0, ph, phs, D), 2 * pts},
-                        RowSpan{q, T, 2 * span(1, 0, qh, qhs, D), 2 * qts});
+    if (!rows_overlap(RowSpan{p.base, T, 2 * token_span(p.heads, p.head_stride, D), 2 * p.token_stride},
+                      RowSpan{q.base, T, 2 * token_span(q.heads, q.head_stride, D), 2 * q.token_stride}))
+        return false;
+    const int64_t hs = p.head_stride;
+    if (hs != q.head_stride || hs < 2 * D || p.token_stride % hs || q.token_stride % hs) return true;
+    const int64_t gap = (int64_t)(reinterpret_cast<uintptr_t>(q.base) - reinterpret_cast<uintptr_t>(p.base));
+    const int64_t d = (gap % (2 * hs) + 2 * hs) % (2 * hs);
+    return d < 2 * D || d + 2 * D > 2 * hs;
 }
 
 int check_heads(const adafuse_heads* m, int64_t T, int32_t D)
@@ -461,8 +472,8 @@ int check_heads(const adafuse_heads* m, int64_t T, int32_t D)
         if (!plain_stride(ld)) return ADAFUSE_ERR_UNSUPPORTED;
     // the outputs of two heads or tokens may not meet: either axis may be the outer one
     const int64_t ts = m->out_token_stride, hs = m->out_head_stride;
-    const bool token_outer = (m->heads == 1 || hs >= D) && (T == 1 || ts >= span(1, 0, m->heads, hs, D));
-    const bool head_outer = (T == 1 || ts >= D) && (m->heads == 1 || hs >= (T - 1) * ts + D);
+    const bool token_outer = (m->heads == 1 || hs >= D) && (T == 1 || ts >= token_span(m->heads, hs, D));
+    const bool head_outer = (T == 1 || ts >= D) && (m->heads == 1 || hs >= (__int128)(T - 1) * ts + D);
     if (!token_outer && !head_outer) return ADAFUSE_ERR_INVALID_ARG;
     return ADAFUSE_OK;
 }
@@ -487,18 +498,25 @@ extern "C" int adafuse_rotary(const adafuse_heads* q, const adafuse_heads* k, in
     if (rot && (!positions || !freq || !aligned_to(positions, ps) || !aligned_to(freq, 8)))
         return ADAFUSE_ERR_INVALID_ARG;
     const adafuse_heads* all[2] = {q, k};
+    const auto span_of = [T, head_dim](const adafuse_heads* m, bool out) {      // strides that are not used: as if dense
+        Span s{out ? m->out : m->in, out ? m->out_token_stride : m->in_token_stride,
+               out ? m->out_head_stride : m->in_head_stride, m->heads};
+        if (m->heads == 1) s.head_stride = head_dim;
+        if (T == 1) s.token_stride = token_span(m->heads, s.head_stride, head_dim);
+        return s;
+    };
     for (int i = 0; i < 2; ++i) {
         const adafuse_heads* o = all[i];
         if (!o) continue;
-        const RowSpan mine{o->out, T, 2 * span(1, 0, o->heads, o->out_head_stride, head_dim), 2 * o->out_token_stride};
+        const Span so = span_of(o, true);
+        const RowSpan mine{o->out, T, 2 * token_span(o->heads, so.head_stride, head_dim), 2 * so.token_stride};
         for (int j = 0; j < 2; ++j) {
             const adafuse_heads* m = all[j];
             if (!m) continue;
-            const bool same = i == j && m->in == o->out && m->in_token_stride == o->out_token_stride &&
-                              m->in_head_stride == o->out_head_stride;
-            if (!same && heads_overlap(o->out, o->out_token_stride, o->out_head_stride, o->heads, m->in,
-                                       m->in_token_stride, m->in_head_stride, m->heads, T, head_dim))
-                return ADAFUSE_ERR_INVALID_ARG;
+            const Span si = span_of(m, false);
+            const bool same = i == j && si.base == so.base && si.token_stride == so.token_stride &&
+                              si.head_stride == so.head_stride;
+            if (!same && heads_overlap(so, si, T, head_dim)) return ADAFUSE_ERR_INVALID_ARG;
             if (m->weight && rows_overlap(mine, RowSpan{m->weight, 1, 2 * head_dim, 2 * head_dim}))
                 return ADAFUSE_ERR_INVALID_ARG;
         }
@@ -506,9 +524,7 @@ extern "C" int adafuse_rotary(const adafuse_heads* q, const adafuse_heads* k, in
                     rows_overlap(mine, RowSpan{freq, 1, 4 * (int64_t)rot, 4 * (int64_t)rot})))
             return ADAFUSE_ERR_INVALID_ARG;
     }
-    if (k && heads_overlap(q->out, q->out_token_stride, q->out_head_stride, q->heads, k->out, k->out_token_stride,
-                           k->out_head_stride, k->heads, T, head_dim))
-        return ADAFUSE_ERR_INVALID_ARG;
+    if (k && heads_overlap(span_of(q, true), span_of(k, true), T, head_dim)) return ADAFUSE_ERR_INVALID_ARG;
 
     const auto heads = [](const adafuse_heads* m) {
         return Heads{static_cast<const uint16_t*>(m->in), static_cast<uint16_t*>(m->out),

@@ -346,8 +346,8 @@ ADAFUSE_API int adafuse_round_bf16(const float* in, void* out, int64_t n, adafus
  * 16-byte aligned.
  * Errors: INVALID_ARG (null pointers, T < 0, sizes < 1, unknown flags, a stride
  * shorter than its row with T > 1, overlapping buffers), UNSUPPORTED
- * (alignment, multiples, an activation that is not listed, T over 2^31 - 256, a
- * stride of 2^38 or more), DEVICE, CUDA.
+ * (alignment, multiples, an activation that is not listed, T, d_in or d_out over
+ * 2^31 - 256, a stride of 2^38 or more), DEVICE, CUDA.
  */
 ADAFUSE_API int adafuse_project(const void* x, int64_t T, int32_t d_in, int64_t x_row_stride, const void* W,
                                 int32_t d_out, int64_t w_row_stride, const void* bias, const void* residual,

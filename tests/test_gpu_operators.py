@@ -441,6 +441,24 @@ def test_rotary_in_place_in_a_fused_buffer(am, D, lead):
     assert bool((cache[:, 0] == 7).all()) and bool((cache[:, T + 1:] == 7).all())
 
 
+@pytest.mark.parametrize("T,heads", [(1, 1), (1, 4), (9, 1), (9, 4)])
+def test_rotary_in_place_with_q_k_v_of_a_head_side_by_side(am, T, heads):
+    D = 64
+    buf = rnd(T, heads, 3, D)
+    was = buf.clone()
+    q, k = buf[:, :, 0], buf[:, :, 1]
+    pos, (freq, _) = torch.arange(T, device="cuda") + 5, am.rotary_frequencies(D, device="cuda")
+    want = am.rotary(q, k, pos, freq)
+    am.rotary(q, k, pos, freq, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(buf[:, :, 2], was[:, :, 2])
+    # one token or one head: a stride that is not used says nothing
+    x = rnd(1, 2, D)
+    y = torch.as_strided(x, (1, 2, D), (7 * D, D, 1))
+    want, _ = am.rotary(x, None, pos[:1], freq)
+    am.rotary(x, None, pos[:1], freq, q_out=y)
+    assert torch.equal(x, want)
+
+
 def test_norm_of_zero_tiny_and_huge_heads(am):
     x = torch.zeros(3, 1, 64, dtype=BF16, device="cuda")
     x[1] = 1e-4

@@ -50,7 +50,8 @@ def test_projections_refuse_bad_arguments(am, kw):
 @pytest.mark.parametrize("kw", [
     {"K": 60, "ldx": 60, "ldw": 60}, {"N": 36, "ldy": 36}, {"x": at(0, 8)}, {"W": at(1, 2)}, {"y": at(2, 8)},
     {"ldx": 68}, {"ldw": 70}, {"ldy": 36}, {"flags": 5}, {"flags": 7}, {"T": 1 << 31},
-    {"ldx": 1 << 38}, {"ldw": 1 << 40}, {"ldy": 1 << 60},
+    {"ldx": 1 << 38}, {"ldw": 1 << 40}, {"ldy": 1 << 60}, {"N": (1 << 31) - 8, "ldy": 1 << 32},
+    {"K": (1 << 31) - 8, "ldx": 1 << 32, "ldw": 1 << 32},
 ])
 def test_projections_refuse_what_they_do_not_support(am, kw):
     assert project(am, **kw) == am.ERR_UNSUPPORTED
@@ -126,6 +127,13 @@ def test_rotary_refusals(am):
     assert rotary(am, heads(am), heads(am, src=at(4), out=at(1))) == bad
     assert rotary(am, heads(am), heads(am, src=at(4), out=at(0))) == bad
     assert rotary(am, heads(am), heads(am, src=at(1), out=at(4))) == bad
+    # heads of q and k side by side: windows that cross, a token stride that breaks the pattern
+    side = dict(its=96, ihs=48, ots=96, ohs=48)
+    assert rotary(am, heads(am, src=at(3), out=at(3), **side),
+                  heads(am, src=at(3, 16), out=at(3, 16), **side)) == bad
+    odd = dict(its=100, ihs=48, ots=100, ohs=48)
+    assert rotary(am, heads(am, src=at(3), out=at(3), **odd), heads(am, src=at(3, 40), out=at(3, 40), **odd)) == bad
+    assert rotary(am, heads(am, n=2, ots=1 << 37, ohs=16), T=1 << 30) == bad      # rows that reach over the inputs
     assert rotary(am, ok, T=0) == am.OK
 
 
