@@ -502,7 +502,7 @@ extern "C" int adafuse_rotary(const adafuse_heads* q, const adafuse_heads* k, in
         Span s{out ? m->out : m->in, out ? m->out_token_stride : m->in_token_stride,
                out ? m->out_head_stride : m->in_head_stride, m->heads};
         if (m->heads == 1) s.head_stride = head_dim;
-        if (T == 1) s.token_stride = token_span(m->heads, s.head_stride, head_dim);
+        if (T == 1) s.token_stride = m->heads * s.head_stride;
         return s;
     };
     for (int i = 0; i < 2; ++i) {
