@@ -51,7 +51,10 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     dirs = [inc, sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
             os.path.join(root, "include")]
     tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+    # the system's compiler, whose C++ runtime is the one that torch's libraries
+    # load: one that links a runtime of its own cannot catch their exceptions
+    gxx = "/usr/bin/g++" if os.path.exists("/usr/bin/g++") else "g++"
+    cmd = [gxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f for d in dirs for f in ("-I", d)),
            source, "-o", tmp, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     if verbose:
