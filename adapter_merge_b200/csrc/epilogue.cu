@@ -13,8 +13,8 @@
 #include <cuda_bf16.h>
 
 #include "act.cuh"
-#include "internal.h"
-#include "ptx.cuh"
+#include "ops.h"
+#include "ptx_ops.cuh"
 
 namespace af {
 namespace {

@@ -2,14 +2,12 @@
 // device table of linears, TMA descriptors (built once per plan), the work
 // split of merge and apply, the device status word, and the entry points that
 // launch the kernels.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <atomic>
 #include <cstring>
 #include <new>
 
-#include "internal.h"
+#include "ops.h"
 
 namespace af {
 

@@ -28,16 +28,14 @@
 // 1.6e-5 at 13824).  bf16 outputs round a thousand times coarser; fp32 outputs
 // accumulate parts of at most 512 columns in accumulators of their own, added
 // up in registers.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <atomic>
 #include <cstring>
 
 #include "act.cuh"
-#include "internal.h"
+#include "ops.h"
 #include "project.h"
-#include "ptx.cuh"
+#include "ptx_ops.cuh"
 
 namespace af {
 

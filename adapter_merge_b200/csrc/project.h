@@ -2,7 +2,7 @@
 // checked it, and the tensor maps of its operands.
 #pragma once
 
-#include "internal.h"
+#include "ops.h"
 
 namespace af {
 

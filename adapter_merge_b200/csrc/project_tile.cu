@@ -27,7 +27,7 @@
 
 #include "act.cuh"
 #include "project.h"
-#include "ptx.cuh"
+#include "ptx_ops.cuh"
 
 namespace af {
 namespace {

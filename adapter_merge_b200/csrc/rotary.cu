@@ -20,8 +20,8 @@
 // rotates those it has.  No barrier across warps.
 #include <cuda_bf16.h>
 
-#include "internal.h"
-#include "ptx.cuh"
+#include "ops.h"
+#include "ptx_ops.cuh"
 
 namespace af {
 namespace {
