@@ -1,10 +1,10 @@
 """Python binding of libadafuse.so (the AdaFuse fused gated multi-LoRA path on
 B200).  Argument marshalling only (through ctypes; for the operators between
 the adapted linears, which run once per layer and token, through the extension
-module _binding): every step of the path runs in the CUDA
-kernels behind the C ABI declared in include/adafuse.h.  PyTorch supplies
-device memory and streams.  There is no fallback: if the shared library is
-missing or fails to load, importing the binding's entry points raises.
+module _binding): every step of the path runs in the CUDA kernels behind the C
+ABI declared in include/adafuse.h.  PyTorch supplies device memory and streams.
+There is no fallback: if the shared library is missing or fails to load,
+importing the binding's entry points raises.
 """
 from __future__ import annotations
 
@@ -190,7 +190,8 @@ def round_bf16(src, out=None, stream=None):
 # and, unless `stream` is given, on that device's current stream; a result that
 # the call allocates belongs to the stream it is computed on.  The arguments
 # are checked and passed on by the extension module _binding: bad tensors raise
-# ValueError, the library's error codes AdafuseError.
+# ValueError, the library's error codes AdafuseError.  They are not recorded for
+# a backward pass.
 
 def _operators():
     """The extension module, with the library's entry points installed."""
