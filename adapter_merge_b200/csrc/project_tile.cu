@@ -315,10 +315,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                     if (++s == kStages) { s = 0; lap ^= 1; }
                 }
             }
-            if (__any_sync(0xffffffffu, *(volatile int*)&abort_flag)) {
-                if (elect_one()) tc_commit_pair(&done);
-                mbar_wait_landed(&done, 0);
-            }
+            __syncwarp();
+            if (elect_one()) tc_commit_pair(&done);         // in both CTAs, also after an abort
         }
         __syncwarp();
     } else {
@@ -428,7 +426,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     if (warp >= 2) bulk_wait_group<0>();
     __syncthreads();
     if (threadIdx.x == 0 && *(volatile int*)&abort_flag && a.status) atomicOr(a.status, ADAFUSE_STATUS_TIMEOUT);
-    cluster_sync();
+    // A CTA may leave once nothing of the other can still reach it: the products
+    // have all signalled (after an abort too), and the second CTA's arrivals on
+    // `accempty`, of which nobody waits for the last two, are released here.
+    if (warp == 1) {
+        mbar_wait_landed(&done, 0);
+        __syncwarp();
+    }
+    cluster_sync_release();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, 512);

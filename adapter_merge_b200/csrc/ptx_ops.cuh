@@ -76,8 +76,8 @@ __device__ __forceinline__ uint32_t cluster_rank()
 
 // Every thread of every CTA of the cluster arrives, and waits for the others.
 // Relaxed: it orders no memory (a release would first wait for all accesses of
-// the thread, about 1000 cycles); what crosses CTAs here is ordered by
-// mbarriers and the fence after their initialisation.
+// the thread, about 1000 cycles); what crosses CTAs before it has to be waited
+// for on mbarriers, or be ordered by the fence after their initialisation.
 __device__ __forceinline__ void cluster_arrive()
 {
     __syncwarp();
@@ -93,6 +93,16 @@ __device__ __forceinline__ void cluster_wait()
 __device__ __forceinline__ void cluster_sync()
 {
     cluster_arrive();
+    cluster_wait();
+}
+
+// The same with a release: also what the threads did to another CTA's shared
+// memory (arrivals on its barriers) has happened there.  For the last meeting
+// of a cluster, after which a CTA's shared memory may belong to another.
+__device__ __forceinline__ void cluster_sync_release()
+{
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     cluster_wait();
 }
 
