@@ -3,11 +3,12 @@
 //
 // Angles.  Pair i of the token at position p turns by p * freq[i] radians.
 // For far positions that product loses its fraction in fp32 (at p = 2^20 an
-// fp32 angle is off by up to 1/32 rad), so the frequency is taken as a
-// fraction of a turn with 64 bits after the point, F = freq / (2 pi) * 2^64,
-// and p * F modulo 2^64 is the exact fraction of the last turn, for positions
-// of either sign: one 64-bit integer product instead of a range reduction.
-// The fraction goes to sincospif.
+// fp32 angle is off by up to 1/32 rad) and in the end in fp64 (by 0.06 rad at
+// 2^50).  So the frequency is taken as a fraction of a turn with 128 bits after
+// the point, F = freq / (2 pi) modulo 1, from a product with 1 / (2 pi) in two
+// doubles (off by at most 2^-105 of freq / (2 pi)), and the upper 64 bits of
+// p * F modulo 1 are two integer products, for positions of either sign and no
+// range reduction.  They go to sincospif.
 //
 // HBM-bound for long prompts (each element read and written once), latency
 // for a decode batch.  One warp, or several, take a token: each computes the
@@ -150,20 +151,41 @@ __device__ __forceinline__ float head_sum(const RotArgs& a, float v, int sub, in
     return __shfl_sync(0xffffffffu, v, group * a.lanes & 31);
 }
 
+// A frequency of f >= 0 radians as turns modulo 1, 128 bits after the point.
+struct Turns {
+    uint64_t hi, lo;
+    __device__ __forceinline__ explicit Turns(double f)
+    {
+        constexpr double kC = 0.15915494309189535, kCLow = -9.839338337591243e-18;     // 1 / (2 pi) and what is left of it
+        constexpr double k2p64 = 18446744073709551616.0;
+        double t = f * kC, e = __fma_rn(f, kCLow, __fma_rn(f, kC, -t));                 // t + e turns
+        t -= floor(t);                          // both exact
+        e -= rint(e);
+        const double a = t * k2p64, b = e * k2p64, below = floor(b);
+        hi = __double2ull_rd(a);
+        lo = __double2ull_rd((a - (double)hi) * k2p64);
+        const uint64_t add = __double2ull_rd((b - below) * k2p64);
+        lo += add;
+        hi += (uint64_t)(int64_t)below + (lo < add ? 1u : 0u);
+    }
+    // the last turn of p times it, in 2^-64 turns
+    __device__ __forceinline__ int64_t times(int64_t p) const
+    {
+        return (int64_t)((uint64_t)p * hi + __umul64hi((uint64_t)p, lo) - (p < 0 ? lo : 0ull));
+    }
+};
+
 // The token's sines and cosines times the factor, by one warp.
 __device__ __forceinline__ void turn_token(const RotArgs& a, int64_t t, float* cosv, float* sinv)
 {
     if (!a.half) return;
     const int64_t p = a.pos32 ? (int64_t)static_cast<const int32_t*>(a.pos)[t] : static_cast<const int64_t*>(a.pos)[t];
-    for (int f = threadIdx.x & 31; f < a.half; f += 32) {
-        double turn = a.freq[f] * 0.15915494309189533577;       // 1 / (2 pi)
-        turn -= floor(turn);
-        const uint64_t frac = turn < 1.0 ? __double2ull_rn(turn * 18446744073709551616.0) : 0ull;     // 2^64 turns
-        const int64_t at = (int64_t)((uint64_t)p * frac);
+    for (int i = threadIdx.x & 31; i < a.half; i += 32) {
+        const double f = a.freq[i];
         float s, c;
-        sincospif((float)at * 1.08420217248550443401e-19f, &s, &c);               // 2^-63 half turns
-        cosv[f] = c * a.factor;
-        sinv[f] = s * a.factor;
+        sincospif((float)Turns(fabs(f)).times(p) * 1.08420217248550443401e-19f, &s, &c);        // 2^-63 half turns
+        cosv[i] = c * a.factor;
+        sinv[i] = (f < 0 ? -s : s) * a.factor;
     }
     __syncwarp();
 }

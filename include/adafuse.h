@@ -407,7 +407,8 @@ typedef struct {
  * for the pairs (a, b) = (i, i + rot/2) or, with ADAFUSE_PAIRS, (2i, 2i + 1),
  * i < rot/2; the elements from rot on are not rotated.  Everything between the
  * bf16 input and the one rounding of the output is fp32, the angle excepted:
- * it is reduced to one turn in 64-bit integers, so far positions lose nothing.
+ * it is reduced to one turn in integers, off by at most |positions[t] freq[i]|
+ * 2^-103 rad before it is rounded to fp32, so far positions lose nothing.
  *   q, k       HOST structs; k may be NULL
  *   positions  int64 (ADAFUSE_POS_I32: int32) [T], any sign: rotating by -p
  *              undoes a rotation by p

@@ -2,11 +2,15 @@
 of the activations, far positions, long sums, and calls whose CTAs leave while
 the other one of a pair has just finished.
 """
+from fractions import Fraction
+
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
 BF16, F32, F64 = torch.bfloat16, torch.float32, torch.float64
+HALF = torch.finfo(BF16).eps / 2       # 2^-8
+STEP = 2.0 ** -23
 
 
 @pytest.fixture(scope="module")
@@ -36,3 +40,53 @@ def test_pairs_whose_second_cta_stores_nothing_last(am, T):
         first = f()
         assert all(torch.equal(first, y) for y in [f() for _ in range(40)])
     assert int(status) == 0
+
+
+# ------------------------------------------------------------------ rotation
+
+def arctan_inverse(n, bits):
+    """arctan(1 / n) * 2^bits by its series, a few units of the last place off."""
+    term = (1 << bits) // n
+    total, k = term, 1
+    while term:
+        term //= -n * n
+        k += 2
+        total += term // k
+    return total
+
+
+BITS = 400
+PI = Fraction(4 * (4 * arctan_inverse(5, BITS) - arctan_inverse(239, BITS)), 1 << BITS)    # Machin
+
+
+def angle(p, f):
+    """p f modulo 2 pi, the product and the reduction in rational numbers."""
+    turns = p * Fraction(f) / (2 * PI)
+    return float((turns - round(turns)) * 2 * PI)
+
+
+FAR = [0, 1, -1, 4097, 2 ** 31 - 1, -2 ** 31, 2 ** 33 + 1, 2 ** 40, -2 ** 40 - 7, 2 ** 50, -2 ** 50, 2 ** 53 + 1,
+       3 * 10 ** 18, 2 ** 62, -2 ** 62 + 12345, 2 ** 63 - 1, -2 ** 63]
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("freq", [
+    [10000.0 ** (-i / 64) for i in range(64)], [500000.0 ** (-i / 16) / 8 for i in range(16)],
+    [1.0, -1.0, 0.3, -0.01, 6.283185307179586, -6.283185307179586, 1000.25, 1048575.9, 1e-9, -1e-15, 0.0, 2.0 ** -60],
+    [3.0], [0.1, 0.7, 1.3]])
+def test_rotary_of_far_positions(am, layout, freq):
+    """Every int64 position, against angles reduced in rational numbers: the
+    stated |p f| 2^-103 of the reduction, fp32 sines and cosines (two steps), of
+    an angle rounded to fp32 (half a step of at most pi), two products and a
+    sum, and one rounding to bf16."""
+    n, T = len(freq), len(FAR)
+    x = rnd(T, 2, 2 * n, seed=n)
+    pos = torch.tensor(FAR, device="cuda")
+    f = torch.tensor(freq, dtype=F64, device="cuda")
+    y, _ = am.rotary(x, None, pos, f, layout=layout)
+    turn = torch.tensor([[angle(p, v) for v in freq] for p in FAR], dtype=F64, device="cuda")[:, None, :]
+    a, b = (slice(0, n), slice(n, 2 * n)) if layout == "half" else (slice(0, 2 * n, 2), slice(1, 2 * n, 2))
+    p, q = x[..., a].to(F64), x[..., b].to(F64)
+    for got, want in ((y[..., a], p * turn.cos() - q * turn.sin()), (y[..., b], p * turn.sin() + q * turn.cos())):
+        err = (8 * STEP + (pos.to(F64)[:, None] * f).abs()[:, None, :] * 2.0 ** -103) * (p.abs() + q.abs())
+        assert bool(((got.to(F64) - want).abs() <= err + HALF * (want.abs() + err)).all())
