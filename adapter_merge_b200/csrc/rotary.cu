@@ -184,6 +184,7 @@ __device__ __forceinline__ void turn_token(const RotArgs& a, int64_t t, float* c
         const double f = a.freq[i];
         float s, c;
         sincospif((float)Turns(fabs(f)).times(p) * 1.08420217248550443401e-19f, &s, &c);        // 2^-63 half turns
+        if (!isfinite(f)) s = c = __int_as_float(0x7fffffff);   // NaN, as the formula has it, at every position
         cosv[i] = c * a.factor;
         sinv[i] = (f < 0 ? -s : s) * a.factor;
     }

@@ -413,7 +413,8 @@ typedef struct {
  *   positions  int64 (ADAFUSE_POS_I32: int32) [T], any sign: rotating by -p
  *              undoes a rotation by p
  *   freq       fp64 [rot/2], radians per position, as adafuse's callers scale
- *              them for long contexts;  factor scales the rotated elements
+ *              them for long contexts (infinite or NaN: its pairs become NaN);
+ *              factor scales the rotated elements
  * Outputs may not overlap inputs other than their own, nor each other (both
  * may live in one buffer, e.g. rows that hold q, k and v of a token).
  * Errors: INVALID_ARG (null pointers, sizes, unknown flags, overlapping

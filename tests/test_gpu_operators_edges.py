@@ -90,3 +90,19 @@ def test_rotary_of_far_positions(am, layout, freq):
     for got, want in ((y[..., a], p * turn.cos() - q * turn.sin()), (y[..., b], p * turn.sin() + q * turn.cos())):
         err = (8 * STEP + (pos.to(F64)[:, None] * f).abs()[:, None, :] * 2.0 ** -103) * (p.abs() + q.abs())
         assert bool(((got.to(F64) - want).abs() <= err + HALF * (want.abs() + err)).all())
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("D", [8, 64, 7])
+def test_frequencies_that_are_no_numbers_reach_their_own_pairs(am, layout, D):
+    x, pos = rnd(5, 3, D), torch.tensor([0, 1, -3, 2 ** 40, 7], device="cuda")
+    n = D // 2 if D % 2 == 0 else 2
+    f = torch.full((n,), 0.25, dtype=F64, device="cuda")
+    good, _ = am.rotary(x, None, pos, f, layout=layout)
+    for i, bad in enumerate((float("nan"), float("inf"), -float("inf"))):
+        g = f.clone()
+        g[i % n] = bad
+        y, _ = am.rotary(x, None, pos, g, layout=layout)
+        pair = [i % n, i % n + n] if layout == "half" else [2 * (i % n), 2 * (i % n) + 1]
+        rest = [j for j in range(D) if j not in pair]
+        assert bool(y[..., pair].isnan().all()) and torch.equal(y[..., rest], good[..., rest])
