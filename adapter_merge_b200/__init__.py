@@ -275,8 +275,10 @@ def rotary_frequencies(dim: int, base: float = 10000.0, scaling: Optional[str] =
       "wavelength"  by the turns that a pair makes within original_length
                     positions: at least fast_turns keeps its frequency, at most
                     slow_turns is slowed by the factor, a linear ramp over the
-                    pairs between; rotated values are scaled by
-                    0.1 ln(factor) + 1 (Peng et al. 2023, "YaRN")."""
+                    pairs between, whose end may lie beyond the slowest pair
+                    (and whose start is the first one at the earliest); rotated
+                    values are scaled by 0.1 ln(factor) + 1 (Peng et al. 2023,
+                    "YaRN").  Needs a base above 1."""
     import math
 
     import torch
@@ -293,12 +295,13 @@ def rotary_frequencies(dim: int, base: float = 10000.0, scaling: Optional[str] =
     if scaling == "linear":
         freq = freq / factor
     elif scaling == "wavelength":
-        if base == 1 or original_length < 1 or not fast_turns > slow_turns > 0:
-            raise ValueError("scaling by wavelength needs a base other than 1, original_length >= 1 and "
+        if base <= 1 or original_length < 1 or not fast_turns > slow_turns > 0:
+            raise ValueError("scaling by wavelength needs a base above 1, original_length >= 1 and "
                              "fast_turns > slow_turns > 0")
         pair = lambda turns: dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
-        lo, hi = max(math.floor(pair(fast_turns)), 0), min(math.ceil(pair(slow_turns)), dim // 2 - 1)
-        ramp = ((i / 2 - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        lo, hi = max(math.floor(pair(fast_turns)), 0), math.ceil(pair(slow_turns))
+        # hi <= 0: even the first pair makes at most slow_turns
+        ramp = ((i / 2 - lo) / max(hi - lo, 1e-3)).clamp(0, 1) if hi > 0 else torch.ones_like(i)
         freq = freq / factor * ramp + freq * (1 - ramp)
         mult = 0.1 * math.log(factor) + 1 if factor > 1 else 1.0
     elif scaling not in (None, "base"):

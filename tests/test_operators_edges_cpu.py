@@ -1,0 +1,48 @@
+"""What of the operators between the adapted linears needs no device, at the
+ends of its range."""
+import math
+
+import pytest
+import torch
+
+import adapter_merge_b200 as am
+
+
+@pytest.mark.parametrize("dim", [2, 8, 64, 128, 256])
+@pytest.mark.parametrize("base", [1.5, 100.0, 10000.0, 500000.0])
+@pytest.mark.parametrize("length", [1, 4, 64, 4096, 65536, 131072, 10 ** 7])
+@pytest.mark.parametrize("fast,slow", [(32.0, 1.0), (4.0, 0.5)])
+def test_wavelength_scaling_by_the_turns_of_each_pair(dim, base, length, fast, slow):
+    """Each pair by its own turns: at least `fast` keeps its frequency, at most
+    `slow` is slowed by the whole factor, and between them the share falls
+    along the pairs by one step each, from a whole pair outside to one outside."""
+    factor = 8.0
+    w, mult = am.rotary_frequencies(dim, base=base, scaling="wavelength", factor=factor, original_length=length,
+                                    fast_turns=fast, slow_turns=slow)
+    assert mult == pytest.approx(0.1 * math.log(factor) + 1)
+    index = lambda turns: dim * math.log(length / (turns * 2 * math.pi), base) / 2      # the pair that makes so many
+    for i in range(dim // 2):
+        f = base ** (-2 * i / dim)
+        turns = length * f / (2 * math.pi)
+        share = (1 - float(w[i]) / f) / (1 - 1 / factor)        # 0: kept, 1: slowed by the whole factor
+        if turns >= fast:
+            assert share == pytest.approx(0, abs=1e-12)
+        elif turns <= slow:
+            assert share == pytest.approx(1, abs=1e-12)
+        else:
+            lo, hi = max(math.floor(index(fast) + 1e-9), 0), math.ceil(index(slow) - 1e-9)
+            assert share == pytest.approx((i - lo) / (hi - lo), abs=1e-9)
+
+
+def test_wavelength_scaling_of_long_contexts():
+    """The slowest pair of 128 turns 2.41 times within 131072 positions: pair 63
+    of a ramp from 45 to 70, not its end."""
+    w, _ = am.rotary_frequencies(128, scaling="wavelength", factor=8.0, original_length=131072)
+    f, _ = am.rotary_frequencies(128)
+    assert float(w[63] / f[63]) == pytest.approx(1 - 18 / 25 * 7 / 8, abs=1e-12)
+
+
+@pytest.mark.parametrize("base", [1.0, 0.5])
+def test_wavelength_scaling_needs_frequencies_that_fall(base):
+    with pytest.raises(ValueError):
+        am.rotary_frequencies(64, base=base, scaling="wavelength", factor=2.0)
