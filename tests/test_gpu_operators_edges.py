@@ -106,3 +106,50 @@ def test_frequencies_that_are_no_numbers_reach_their_own_pairs(am, layout, D):
         pair = [i % n, i % n + n] if layout == "half" else [2 * (i % n), 2 * (i % n) + 1]
         rest = [j for j in range(D) if j not in pair]
         assert bool(y[..., pair].isnan().all()) and torch.equal(y[..., rest], good[..., rest])
+
+
+# ------------------------------------------------------------------ activations
+
+def act64(v, name):
+    """Without cancellation or overflow in the tails."""
+    if name == "gelu":
+        return 0.5 * v * torch.special.erfc(-v / 2 ** 0.5)
+    w = v if name == "silu" else (8 / torch.pi) ** 0.5 * (v + 0.044715 * v ** 3)
+    return v * torch.special.expit(w)
+
+
+def act_error(v, name):
+    """Relative error of an activation in fp32, in units of 2^-23.
+    gelu, v Q(v) with Q(-|v|) = exp(-v^2 / 2) t P(t): the square's rounding is
+    0.25 v^2 in the exponent, __expf is off by 2 + 1.173 v^2 / 2 (its documented
+    bound); t by 2.5 (a sum and __fdividef's 2), which counts up to 1.1 times;
+    P by 0.3 of its fit and 2 of its rounding; three products: 0.84 v^2 + 10."""
+    assert name == "gelu"
+    return (0.84 * v * v + 10) * STEP
+
+
+TAILS = {"gelu": (-12.8, 14.0)}
+
+
+@pytest.mark.parametrize("name", list(TAILS))
+def test_activations_keep_their_digits_in_the_tails(am, name):
+    """Relative to the result, down to where it leaves fp32's normal numbers."""
+    lo, hi = TAILS[name]
+    v = torch.linspace(lo, hi, 1 << 16, device="cuda", dtype=F32).view(256, 256)
+    want = act64(v.to(F64), name)
+    rel = act_error(v.to(F64), name)
+    y = am.epilogue(v, activation=name, out_dtype=F32)
+    assert bool(((y.to(F64) - want).abs() <= rel * want.abs() + 2.0 ** -126).all())
+    y = am.epilogue(v, activation=name)
+    assert bool(((y.to(F64) - want).abs() <= (rel + HALF * (1 + rel)) * want.abs() + 2.0 ** -126).all())
+    # the same behind products with a one in each row, of values that bf16 holds
+    b = v.to(BF16).view(512, 128)
+    eye = torch.eye(128, dtype=BF16, device="cuda")
+    want, rel = act64(b.to(F64), name), act_error(b.to(F64), name)
+    for T in (5, 512):
+        bound = rel[:T] * want[:T].abs() + 2.0 ** -126
+        y = am.project(b[:T], eye, activation=name, out_dtype=F32)
+        assert bool(((y.to(F64) - want[:T]).abs() <= bound).all())
+        y = am.gated_project(b[:T], eye, torch.zeros_like(eye), activation=name,
+                             bias_up=torch.ones(128, dtype=BF16, device="cuda"))
+        assert bool(((y.to(F64) - want[:T]).abs() <= bound + HALF * (1 + rel[:T]) * want[:T].abs()).all())
