@@ -123,15 +123,23 @@ def act_error(v, name):
     gelu, v Q(v) with Q(-|v|) = exp(-v^2 / 2) t P(t): the square's rounding is
     0.25 v^2 in the exponent, __expf is off by 2 + 1.173 v^2 / 2 (its documented
     bound); t by 2.5 (a sum and __fdividef's 2), which counts up to 1.1 times;
-    P by 0.3 of its fit and 2 of its rounding; three products: 0.84 v^2 + 10."""
-    assert name == "gelu"
-    return (0.84 * v * v + 10) * STEP
+    P by 0.3 of its fit and 2 of its rounding; three products: 0.84 v^2 + 10.
+    silu and gelu_tanh, v / (1 + exp(-w)): __expf is off by 2 + 1.173 |w|, its
+    product and the sum by 0.5 each, the division by 2; where exp(-|w|) is below
+    2^-126 it is a multiple of 2^-149 (one of at least 2^13 of them here) and off
+    by another 2^10.  gelu_tanh's w is off by 3 relative (a square, a product, a
+    sum with a share of both, two products: 0.5 each, and its two constants')."""
+    if name == "gelu":
+        return (0.84 * v * v + 10) * STEP
+    w = v if name == "silu" else (8 / torch.pi) ** 0.5 * (v + 0.044715 * v ** 3)
+    e = (1.173 if name == "silu" else 1.173 + 3.5) * w.abs() + 7
+    return (e + torch.where(w < -87.3, 1024.0, 0.0)) * STEP
 
 
-TAILS = {"gelu": (-12.8, 14.0)}
+TAILS = {"gelu": (-12.8, 14.0), "silu": (-91.5, 100.0), "gelu_tanh": (-10.3, 14.0)}
 
 
-@pytest.mark.parametrize("name", list(TAILS))
+@pytest.mark.parametrize("name", TAILS)
 def test_activations_keep_their_digits_in_the_tails(am, name):
     """Relative to the result, down to where it leaves fp32's normal numbers."""
     lo, hi = TAILS[name]
