@@ -24,10 +24,13 @@
 // load's way (1.2 us) and the sum over the cluster (1 us) are not hidden.
 //
 // The tensor core rounds each step of an accumulator towards zero, which adds
-// up over long sums (measured against 64 bits: 4.4e-6 relative at d_in = 4096,
-// 1.6e-5 at 13824).  bf16 outputs round a thousand times coarser; fp32 outputs
-// accumulate parts of at most 512 columns in accumulators of their own, added
-// up in registers.
+// up over long sums: about 1e-9 d_in of the result (measured against 64 bits:
+// 4.4e-6 at d_in = 4096, 1.6e-5 at 13824, 1.2e-4 at 131072, where all products
+// have one sign).  bf16 outputs, off by 2^-9 to 2^-8 from their one rounding,
+// keep one accumulator per multiplying warp, and d_in is limited to kMaxSum for
+// them, where the sums' error is a sixteenth of that; fp32 outputs accumulate
+// parts of at most 512 columns in accumulators of their own, added up in
+// registers, for any d_in.
 #include <algorithm>
 #include <atomic>
 #include <cstring>
@@ -55,6 +58,7 @@ namespace {
 constexpr int kStreamThreads = 256;                     // one warp loads, two multiply; all finish
 constexpr int kMaxRing = 12;                            // stages of at least 18 KB
 constexpr int kMaxSplits = 8;
+constexpr int32_t kMaxSum = 131072;                     // most columns of a bf16 output's sum
 constexpr uint32_t kWTile = kTileM * kChunkK * 2;       // 16 KB
 
 struct StreamArgs : ProjectArgs {
@@ -480,7 +484,7 @@ int check(ProjectCall& c, const void* bias, const void* bias_up, bool gated, uin
     if (flags & ~(ADAFUSE_ACT_MASK | ADAFUSE_TEST_STALL | (gated ? 0u : ADAFUSE_OUT_F32))) return ADAFUSE_ERR_INVALID_ARG;
     if (a.T < 0 || c.K < 1 || a.N < 1) return ADAFUSE_ERR_INVALID_ARG;
     if (act > ADAFUSE_ACT_GELU_TANH || c.K % 8 || a.N % 8 || a.T > 0x7fffff00 || a.N > 0x7fffff00 ||
-        c.K > 0x7fffff00) return ADAFUSE_ERR_UNSUPPORTED;
+        c.K > (flags & ADAFUSE_OUT_F32 ? 0x7fffff00 : kMaxSum)) return ADAFUSE_ERR_UNSUPPORTED;
     if (a.T == 0) return ADAFUSE_OK;
     if (!c.x || !c.W || !a.y || (gated && !c.W_up)) return ADAFUSE_ERR_INVALID_ARG;
     a.y_f32 = flags & ADAFUSE_OUT_F32 ? 1 : 0;

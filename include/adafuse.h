@@ -333,9 +333,11 @@ ADAFUSE_API int adafuse_round_bf16(const float* in, void* out, int64_t n, adafus
 /*
  * Projection: y[t, :] = act(x[t, :] W^T + bias) + residual[t, :], the products
  * and everything after them in fp32, rounded once to bf16 (with
- * ADAFUSE_OUT_F32 not at all: a row-parallel rank's partial sums; sums over
- * more than 512 columns are then added up in parts, so that the result keeps
- * close to fp32's precision).
+ * ADAFUSE_OUT_F32 not at all: a row-parallel rank's partial sums).  The tensor
+ * core rounds each step of a sum towards zero, together by about d_in 2^-30 of
+ * the sum of the products' magnitudes; with ADAFUSE_OUT_F32 sums over more than
+ * 512 columns are added up in parts, so that the result keeps close to fp32's
+ * precision.
  *   x         bf16 [T, d_in], rows x_row_stride elements apart
  *   W         bf16 [d_out, d_in], rows w_row_stride apart: e.g. a W_out that
  *             adafuse_merge wrote
@@ -351,7 +353,8 @@ ADAFUSE_API int adafuse_round_bf16(const float* in, void* out, int64_t n, adafus
  * Errors: INVALID_ARG (null pointers, T < 0, sizes < 1, unknown flags, a stride
  * shorter than its row with T > 1, overlapping buffers), UNSUPPORTED
  * (alignment, multiples, an activation that is not listed, T, d_in or d_out over
- * 2^31 - 256, a stride of 2^38 or more), DEVICE, CUDA.
+ * 2^31 - 256, d_in over 131072 with a bf16 result, a stride of 2^38 or more),
+ * DEVICE, CUDA.
  */
 ADAFUSE_API int adafuse_project(const void* x, int64_t T, int32_t d_in, int64_t x_row_stride, const void* W,
                                 int32_t d_out, int64_t w_row_stride, const void* bias, const void* residual,

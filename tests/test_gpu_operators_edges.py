@@ -161,3 +161,30 @@ def test_activations_keep_their_digits_in_the_tails(am, name):
         y = am.gated_project(b[:T], eye, torch.zeros_like(eye), activation=name,
                              bias_up=torch.ones(128, dtype=BF16, device="cuda"))
         assert bool(((y.to(F64) - want[:T]).abs() <= bound + HALF * (1 + rel[:T]) * want[:T].abs()).all())
+
+
+# ------------------------------------------------------------------ long sums
+
+@pytest.mark.parametrize("T,N", [(16, 512), (300, 256)])
+def test_longest_sums(am, T, N):
+    """Sums of products of one sign, whose partial sums are as large as they can
+    be, by the accumulator's rounding towards zero: at most a sixteenth of a
+    bf16 rounding of 2^-8 for the longest that are taken.  Projected onto the
+    exact results, with rows of every scale within a step, the roundings
+    themselves average out (each uniform in 2^-8 of its value: 1.1e-3 / sqrt(TN)
+    = 1.3e-5)."""
+    K = 131072
+    scale = 1 + torch.rand(T, 1, device="cuda", generator=torch.Generator("cuda").manual_seed(T))
+    x = (rnd(T, K, dtype=F32).abs() * scale).to(BF16)
+    W = rnd(N, K, seed=1, std=0.02).abs()
+    want = sum(x[:, k:k + 16384].to(F64) @ W[:, k:k + 16384].to(F64).t() for k in range(0, K, 16384))
+    off = lambda y: float((y.to(F64) * want).sum() / (want * want).sum() - 1)
+    one = torch.ones(N, dtype=BF16, device="cuda")
+    assert abs(off(am.project(x, W))) < HALF / 16
+    assert abs(off(am.gated_project(x, torch.zeros_like(W), W, bias_gate=one, activation="relu"))) < HALF / 16
+    assert abs(off(am.project(x, W, out_dtype=F32))) < 1.5e-6
+    x, W = torch.cat([x, x], 1), torch.cat([W, W], 1)
+    assert abs(off(am.project(x, W, out_dtype=F32) / 2)) < 1.5e-6
+    for call in (lambda: am.project(x, W), lambda: am.gated_project(x, W, W)):
+        with pytest.raises(am.AdafuseError):
+            call()

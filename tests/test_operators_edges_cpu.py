@@ -46,3 +46,30 @@ def test_wavelength_scaling_of_long_contexts():
 def test_wavelength_scaling_needs_frequencies_that_fall(base):
     with pytest.raises(ValueError):
         am.rotary_frequencies(64, base=base, scaling="wavelength", factor=2.0)
+
+
+# ------------------------------------------------------------------ refusals
+
+@pytest.fixture(scope="module")
+def lib():
+    from adapter_merge_b200 import build
+    build.build()
+    return am.lib()
+
+
+def at(i):
+    """A made-up device address, 1 TiB apart (nothing is read before a launch)."""
+    return (i + 1) << 40
+
+
+def test_sums_too_long_for_one_accumulator_are_refused(lib):
+    """bf16 results keep one fp32 accumulator that rounds towards zero; fp32
+    results add up parts, and take any d_in (refused further on, without a device)."""
+    project = lambda K, flags: lib.adafuse_project(at(0), 4, K, K, at(1), 32, K, None, None, 0, at(2), 32, flags, None,
+                                                   None)
+    gated = lambda K: lib.adafuse_gated_project(at(0), 4, K, K, at(1), at(3), 32, K, None, None, at(2), 32, 2, None,
+                                                None)
+    for K in (131080, 1 << 20):
+        assert project(K, 0) == project(K, 1) == gated(K) == am.ERR_UNSUPPORTED
+    if not torch.cuda.is_available():
+        assert project(131072, 0) == gated(131072) == project(1 << 20, am.OUT_F32) == am.ERR_DEVICE
