@@ -20,7 +20,6 @@ __all__ = [
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libadafuse.so")
-_BINDING_PATH = os.path.join(_HERE, "_binding.so")
 
 OK = 0
 ERR_INVALID_ARG = 1
@@ -200,10 +199,13 @@ def _operators():
         import importlib.util
 
         import torch  # noqa: F401  (its libraries, which the module links)
-        L = lib()
-        if not os.path.exists(_BINDING_PATH):
-            raise RuntimeError(f"_binding.so not built ({_BINDING_PATH}); run adapter_merge_b200.build.build()")
-        spec = importlib.util.spec_from_file_location(__name__ + "._binding", _BINDING_PATH)
+
+        from .build import binding_path
+        L, path = lib(), binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"the operators' binding is not built for this Python and torch ({path}); run "
+                               "adapter_merge_b200.build.build()")
+        spec = importlib.util.spec_from_file_location(__name__ + "._binding", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         module.install(*(ctypes.cast(f, ctypes.c_void_p).value for f in (

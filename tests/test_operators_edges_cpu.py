@@ -1,11 +1,15 @@
 """What of the operators between the adapted linears needs no device, at the
 ends of its range."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
 import adapter_merge_b200 as am
+from adapter_merge_b200 import build as ambuild
 
 
 @pytest.mark.parametrize("dim", [2, 8, 64, 128, 256])
@@ -52,8 +56,7 @@ def test_wavelength_scaling_needs_frequencies_that_fall(base):
 
 @pytest.fixture(scope="module")
 def lib():
-    from adapter_merge_b200 import build
-    build.build()
+    ambuild.build()
     return am.lib()
 
 
@@ -73,3 +76,50 @@ def test_sums_too_long_for_one_accumulator_are_refused(lib):
         assert project(K, 0) == project(K, 1) == gated(K) == am.ERR_UNSUPPORTED
     if not torch.cuda.is_available():
         assert project(131072, 0) == gated(131072) == project(1 << 20, am.OUT_F32) == am.ERR_DEVICE
+
+
+# ------------------------------------------------------------------ build
+
+def recorded(monkeypatch, tmp_path, fail=None):
+    """Builds into tmp_path by a compiler that only writes its output; the commands."""
+    ran = []
+    tmp_path = tmp_path / "package"
+    tmp_path.mkdir()
+    (tmp_path.parent / "include").mkdir()
+    (tmp_path.parent / "include" / "adafuse.h").touch()
+
+    def run(cmd):
+        if fail and fail in os.path.basename(cmd[0]):
+            raise subprocess.CalledProcessError(1, cmd)
+        ran.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+
+    monkeypatch.setattr(ambuild, "HERE", str(tmp_path))
+    monkeypatch.setattr(ambuild, "LIB", str(tmp_path / "libadafuse.so"))
+    monkeypatch.setattr(ambuild.subprocess, "check_call", run)
+    return ran
+
+
+def test_the_library_is_built_without_torch_or_a_host_compiler(monkeypatch, tmp_path):
+    ran = recorded(monkeypatch, tmp_path, fail="g++")
+    with pytest.raises(subprocess.CalledProcessError):
+        ambuild.build()
+    assert len(ran) == 1 and os.path.exists(ambuild.LIB)
+    ran.clear()
+    monkeypatch.setitem(sys.modules, "torch", None)
+    assert ambuild.build(force=True) == ambuild.LIB
+    assert len(ran) == 1 and "nvcc" in ran[0][0]
+
+
+def test_a_binding_serves_the_torch_that_it_was_built_for(monkeypatch, tmp_path):
+    ran = recorded(monkeypatch, tmp_path)
+    first = ambuild.build_binding()
+    assert ambuild.build_binding() == first and len(ran) == 1
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    assert not os.path.exists(ambuild.binding_path())
+    monkeypatch.setattr(am, "_native", None)
+    monkeypatch.setattr(am, "lib", lambda: None)
+    with pytest.raises(RuntimeError, match="not built"):
+        am._operators()
+    second = ambuild.build_binding()
+    assert second != first and len(ran) == 2
