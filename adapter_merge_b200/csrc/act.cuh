@@ -26,8 +26,8 @@ __device__ __forceinline__ float gate_by(float v, float w)
 // Shepherd and Laframboise 1981): t P(t), with P of degree 8 fitted to the
 // smallest relative error over x < 14.5, 2.6e-8.  No branch; relative to the
 // result it is off by (0.84 v^2 + 10) 2^-23 at most, the first part from the
-// exponential.  An epilogue of 2047 x 13824 bf16 takes 46-53 us with it (49-52
-// with erff, 64 with erfcf), bound by instructions; silu 30.
+// exponential.  An epilogue of 2047 x 13824 bf16 takes 45-49 us with it (49-51
+// with erff, 64 with erfcf), bound by instructions; silu 32.
 __device__ __forceinline__ float gelu(float v)
 {
     const float t = __fdividef(1.f, fmaf(0.34375f, fabsf(v), 1.f));
