@@ -189,8 +189,9 @@ def round_bf16(src, out=None, stream=None):
 # and, unless `stream` is given, on that device's current stream; a result that
 # the call allocates belongs to the stream it is computed on.  The arguments
 # are checked and passed on by the extension module _binding: bad tensors raise
-# ValueError, the library's error codes AdafuseError.  They are not recorded for
-# a backward pass.
+# ValueError, the library's error codes AdafuseError.  They have no backward
+# pass: a tensor that requires grad is taken as its values, and no result has a
+# gradient function.
 
 def _operators():
     """The extension module, with the library's entry points installed."""
@@ -232,7 +233,8 @@ def project(x, W, bias=None, activation=None, residual=None, out=None, out_dtype
     `out` itself).  activation: "relu", "silu", "gelu", "gelu_tanh" or None.
     Returns `out`, bf16 [T, d_out]; out_dtype=torch.float32 leaves the fp32
     result unrounded (a row-parallel rank's partial sums).  STATUS_TIMEOUT is
-    OR-ed into `status` (int32 [1]) when a device-side wait gave up."""
+    OR-ed into `status` (int32 [1]) when a device-side wait gave up.  Forward
+    only: gradients do not pass through the call."""
     r = (_native or _operators()).project(x, W, bias, _activation(activation), residual, out, out_dtype, status,
                                           _raw(stream))
     if r.__class__ is int:
@@ -244,7 +246,8 @@ def gated_project(x, W_gate, W_up, bias_gate=None, bias_up=None, activation="sil
                   stream=None):
     """act(x W_gate^T + bias_gate) * (x W_up^T + bias_up) in one launch: the
     feed-forward block's two projections, activation and product.  Weights bf16
-    [d_out, d_in] with the same row stride; everything else as project."""
+    [d_out, d_in] with the same row stride; everything else as project.  Forward
+    only: gradients do not pass through the call."""
     r = (_native or _operators()).gated_project(x, W_gate, W_up, bias_gate, bias_up, _activation(activation), out,
                                                 status, _raw(stream))
     if r.__class__ is int:
@@ -258,7 +261,8 @@ def epilogue(y, bias=None, activation=None, up=None, residual=None, out=None, ou
     output plus the residual stream, or all-reduced fp32 sums.  y and up
     [T, n], both bf16 or both fp32; bias bf16 [n]; residual bf16 [T, n].  Rows
     may be strided, those of y, up and residual one expanded row.  Returns
-    `out`, bf16 [T, n] (or fp32); it may be y, up or residual itself."""
+    `out`, bf16 [T, n] (or fp32); it may be y, up or residual itself.  Forward
+    only: gradients do not pass through the call."""
     r = (_native or _operators()).epilogue(y, bias, _activation(activation), up, residual, out, out_dtype,
                                            _raw(stream))
     if r.__class__ is int:
@@ -320,7 +324,8 @@ def rotary(q, k, positions, freq, layout: str = "half", factor: float = 1.0, q_w
     elements from rot on are not rotated.  layout "half" rotates elements i and
     i + rot/2, "interleaved" 2i and 2i + 1; `factor` scales the rotated
     elements.  q_weight / k_weight bf16 [D].  Returns (q_out, k_out), new
-    contiguous tensors unless given; q_out may be q itself, k_out k."""
+    contiguous tensors unless given; q_out may be q itself, k_out k.  Forward
+    only: gradients do not pass through the call."""
     if layout not in ("half", "interleaved"):
         raise ValueError(f"layout {layout!r} is neither 'half' nor 'interleaved'")
     r = (_native or _operators()).rotary(q, k, positions, freq, 0 if layout == "half" else PAIRS, factor, q_weight,

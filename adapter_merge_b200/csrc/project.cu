@@ -18,10 +18,10 @@
 // its cluster, so no CTA ever waits for another while it holds TMEM that the
 // other needs.
 //
-// Bound by W's bytes: one token through 4096 -> 11008 gate and up (180 MB) 31.6
-// us, 5.7 TB/s; 64 tokens through 5120 -> 13824 (283 MB) 50.4 us, 5.6 TB/s.  A
-// single 4096 x 4096 layer (33.5 MB, 5.1 us) takes 8.6: the launch, the first
-// load's way (1.2 us) and the sum over the cluster (1 us) are not hidden.
+// Bound by W's bytes: one token through 4096 -> 11008 gate and up (180 MB) 31
+// us, 5.8 TB/s; 64 tokens through 5120 -> 13824 (283 MB) 50-53 us, 5.4-5.7 TB/s.
+// A single 4096 x 4096 layer (33.5 MB, 5.1 us) takes 8.4-8.8: the launch, the
+// first load's way (1.2 us) and the sum over the cluster (1 us) are not hidden.
 //
 // The tensor core rounds each step of an accumulator towards zero, which adds
 // up over long sums: about 1e-9 d_in of the result (measured against 64 bits:

@@ -15,9 +15,11 @@
 //
 // A 64-column chunk of a wide tile takes 505 cycles, the products' own time;
 // beyond a few milliseconds of work the board's power limit sets the clock
-// (1.2-1.5 GHz of 1.97), which is then what bounds the call: 4096 tokens, 11008
-// -> 4096, 300 us (1.23 PFLOP/s; the library's plain product 279 us on such a
-// board), 2001 tokens through the 7B gate and up, 277 us (1.30 PFLOP/s).
+// (1.2-1.5 GHz of 1.97), which then bounds the call together with the last
+// round, in which not all pairs have a tile: 4096 tokens, 11008 -> 4096, 295-313
+// us (1.18-1.25 PFLOP/s; 3.46 rounds run as 4; a library's plain product 279 us),
+// 2001 tokens through the 7B gate and up, 276-283 us (1.28-1.31 PFLOP/s; 9.3
+// rounds run as 10).
 //
 // fp32 outputs take a fresh accumulator every 512 columns of d_in, added up in
 // the epilogue's registers (the tensor core's rounding towards zero adds up

@@ -30,8 +30,9 @@ namespace {
 constexpr int kRotThreads = 128;
 constexpr int kRotWarps = kRotThreads / 32;
 // Heads that a lane loads ahead of those it rotates.  8192 tokens of 32 + 8
-// heads of 128 with norms: 33.3 us with two, 36.9 with one; 4097 tokens of 80
-// heads, interleaved: 30.7 with two (of one vector each).
+// heads of 128 with norms: 33.3 us with two, 36.9 with one (34.3-34.8 now, with
+// angles of 128 bits); 4097 tokens of 80 heads, interleaved: 30.8-31.5 with two
+// (of one vector each).
 __host__ __device__ constexpr int flight(bool pairs, bool norm) { return (norm ? 2 : 1) * (pairs ? 2 : 1); }
 constexpr int kLaneHeads = 20;          // most heads of a prompt's token per lane
 constexpr int kMaxHeadDim = 1024;

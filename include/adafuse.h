@@ -308,8 +308,8 @@ ADAFUSE_API int adafuse_round_bf16(const float* in, void* out, int64_t n, adafus
  * keys (adafuse_rotary).  None has a counterpart on the pages, which decode
  * with the fused weights (page pt section 2.B) and leave the layer to the
  * backbone.  They take no plan and no workspace, run on the current device,
- * are one launch each, and can be captured into a graph.  T == 0 is valid and
- * launches nothing.  An output may not overlap an input, except where a call
+ * are one launch each, and can be captured into a graph.  They are forward
+ * forms, without a backward pass.  T == 0 is valid and launches nothing.  An output may not overlap an input, except where a call
  * says that it may be the same buffer.
  */
 
@@ -416,6 +416,8 @@ typedef struct {
  * bf16 input and the one rounding of the output is fp32, the angle excepted:
  * it is reduced to one turn in integers, off by at most |positions[t] freq[i]|
  * 2^-103 rad before it is rounded to fp32, so far positions lose nothing.
+ * (The squares of a head are summed in fp32: elements beyond 1e17 can overflow
+ * the sum, and the head then becomes 0.)
  *   q, k       HOST structs; k may be NULL
  *   positions  int64 (ADAFUSE_POS_I32: int32) [T], any sign: rotating by -p
  *              undoes a rotation by p
